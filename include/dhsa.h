@@ -32,6 +32,16 @@
  *   for dhsa_last_cuda_error(). Device-side failures (a bounded wait that
  *   timed out, an offsets table found inconsistent) set a device status word
  *   that dhsa_check_device_status() reads; compute calls never trap.
+ * - The calls of sections 6 to 8 work on a key/value cache that follows the
+ *   prefill. Q, K, V and the caches are bf16 with 128-element rows; where a
+ *   call takes `*_strides`, that is a HOST pointer to three int64 (batch, head,
+ *   row; in elements), or NULL for the dense layout. Rows are contiguous;
+ *   strides are multiples of 8 elements and base pointers 16-byte aligned.
+ *     cache K, V  bf16 [B, Hkv, cap, 128]   slot s of kv head h of sequence b
+ *     lengths     int32 [B]  slots 0 .. lengths[b]-1 hold keys; the drafted
+ *                            tokens of a step sit in the slots right after
+ *     n_draft     int32 [B]  drafted (or new) tokens of each sequence, or NULL
+ *   Slots past lengths[b] + n_draft[b] may hold anything, NaN included.
  * - The library holds no per-call state; calls on different streams may run
  *   concurrently as long as their buffers do not overlap.
  */
@@ -61,6 +71,11 @@ typedef enum {
                                           or met (and clamped) by pooling, or met by the attention's
                                           work-list builder (the batch element is then skipped) */
 #define DHSA_DEVFLAG_BAD_SELECTION 0x4 /* the CSR builder met a selected chunk outside [0, i] */
+#define DHSA_DEVFLAG_BAD_CACHE 0x8     /* a cache length or draft count was negative or led past the
+                                          cache's capacity (clamped), or a slot to write lay outside
+                                          the cache (not written) */
+#define DHSA_DEVFLAG_BAD_TREE 0x10     /* a drafted token's parent was neither -1 nor an earlier drafted
+                                          token (taken as -1) */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* dhsa_status_string(int status);
@@ -350,6 +365,111 @@ int dhsa_sparse_attn_fwd_tiles(const void* Q, const void* K, const void* V, int 
  *    limit_ns: 1 .. 100,000,000 for modes 1 and 2 (DHSA_ERR_INVALID_ARG else).
  * ------------------------------------------------------------------------- */
 int dhsa_debug_arm_wait_timeout(int mode, uint64_t limit_ns);
+
+/* ---------------------------------------------------------------------------
+ * 6. Rotary positions, with the append of new keys and values to a cache.
+ *    The pages start from rotated Q and K; this makes them from the
+ *    projections' outputs, for the prefill (1. to 4.) and for each new token.
+ *
+ *    For row (b, h, t) at position p, pairs i = 0 .. rotary_dim/2 - 1:
+ *      a_i = p * inv_freq[i],  c = factor * cos a_i,  s = factor * sin a_i
+ *      (x, y) -> (x c - y s, x s + y c);  transpose != 0: s -> -s (the
+ *      transposed matrix: the gradient of the rotation)
+ *    where (x, y) are elements (i, i + rotary_dim/2) of the row, or
+ *    (2i, 2i + 1) when interleaved != 0; elements from rotary_dim on are
+ *    copied. a_i is reduced modulo one turn in 64-bit integers before the
+ *    fp32 cosine and sine, so far positions keep fp32 accuracy; results are
+ *    rounded once to bf16. Scaled frequencies (long contexts) are the caller's
+ *    inv_freq and factor.
+ *
+ *    Q  [B, Hq, T, 128] (q_strides), K, V [B, Hkv, T, 128] (k_strides,
+ *       v_strides). Q, K or V may be NULL with their output (not all three).
+ *    inv_freq   fp64 [rotary_dim/2] (device, finite); rotary_dim 16 .. 128, a multiple of 16
+ *    position   p = positions[b*T + t] (int32), or start[b] + t when positions
+ *               is NULL, or t when both are.
+ *    n_new      int32 [B] or NULL (T): rows t >= n_new[b] are neither read nor written
+ *    Q_out      dense [B, Hq, T, 128]
+ *    K_out, V_out  [B, Hkv, cap, 128] (ko_strides, vo_strides): row t goes to
+ *               row slots[b] + t (slots NULL: row t). V is copied. A row
+ *               outside [0, cap) is not written (DHSA_DEVFLAG_BAD_CACHE).
+ *    pos_out    int32 [B, Hkv, cap] or NULL: the position, beside each K row
+ *    An output may be its own input (same pointer, same strides, slots NULL);
+ *    otherwise outputs overlap neither inputs nor each other.
+ * ------------------------------------------------------------------------- */
+int dhsa_rotary_qkv(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
+                    const int64_t* v_strides, int B, int Hq, int Hkv, int T, int head_dim, const double* inv_freq,
+                    int rotary_dim, int interleaved, int transpose, float factor, const int32_t* positions,
+                    const int32_t* start, const int32_t* n_new, void* Q_out, void* K_out, const int64_t* ko_strides,
+                    void* V_out, const int64_t* vo_strides, const int32_t* slots, int cap, int32_t* pos_out,
+                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 7. Attention of drafted tokens over a cache.
+ *    The step after the prefill: each sequence has 1 .. 64 new tokens whose K
+ *    and V are already in the cache (6.), in slots lengths[b] + j. They form a
+ *    tree: parents[b*T + t] is the drafted token that t continues, or -1 when
+ *    t continues the cached context; parents NULL is the chain t - 1. One new
+ *    token is plain decoding, a chain of the last prompt tokens scores the
+ *    cache before its first eviction (8.).
+ *
+ *    Token t < n_draft[b] (NULL: T) sees every slot s < lengths[b], itself and
+ *    its ancestors:
+ *      O[b,hq,t,:] = sum_s p_s V[b,hkv,s], p = softmax_s(scale * <Q[b,hq,t], K[b,hkv,s]>)
+ *    fp32 accumulation and softmax statistics, bf16 output.
+ *    Q, O   dense [B, Hq, T, 128], T <= 64, Hq / Hkv <= 64
+ *    lse    fp32 [B, Hq, T] or NULL: natural log of the softmax denominator
+ *    weight / weight_out  fp32 [B, Hkv, cap], both or neither: for s < lengths[b]
+ *             weight_out[s] = weight[s] + sum over the head's Hq/Hkv query
+ *             heads and the drafted tokens of p_s; for a drafted token's slot
+ *             the sum alone. weight_out may be weight.
+ *    Rows t >= n_draft[b] of O and lse and the other slots of weight_out are
+ *    left as they were. lengths[b] outside [0, cap] and n_draft[b] outside
+ *    [0, T] or past the capacity are clamped (DHSA_DEVFLAG_BAD_CACHE); a
+ *    parent outside [-1, t) is taken as -1 (DHSA_DEVFLAG_BAD_TREE).
+ *    V rows of cached and drafted tokens must be finite.
+ *    Results do not depend on what else runs: no atomics on values, one order
+ *    of sums for given lengths. workspace: dhsa_tree_attn_workspace_size(B, Hq,
+ *    Hkv, T, cap, weight != NULL) bytes; it needs no initial contents. Calls that share a
+ *    workspace must not overlap on the GPU.
+ * ------------------------------------------------------------------------- */
+int dhsa_tree_max_drafts(void);
+size_t dhsa_tree_attn_workspace_size(int B, int Hq, int Hkv, int T, int cap, int want_weight);
+int dhsa_tree_attn(const void* Q, const void* K, const int64_t* k_strides, const void* V, const int64_t* v_strides,
+                   int B, int Hq, int Hkv, int T, int cap, int head_dim, const int32_t* lengths,
+                   const int32_t* parents, const int32_t* n_draft, float softmax_scale, void* O, float* lse,
+                   const float* weight, float* weight_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 8. Eviction from a cache by accumulated attention weight, and the commit of
+ *    accepted drafts.
+ *    Candidates of sequence b: slots s < lengths[b], and slots lengths[b] + j
+ *    for j < n_draft[b] with bit j of accept[b] set (accept NULL: all; n_draft
+ *    NULL: none). m = min(keep, candidates). Each kv head keeps its own m
+ *    candidates, ranked by (held first, weight descending, slot ascending);
+ *    held: pos < sinks or pos >= next_pos[b] - recent (next_pos NULL: recent
+ *    must be 0). A NaN weight ranks below every number; -0 equals +0.
+ *
+ *    Kept rows end in slots 0 .. m-1: a kept slot below m stays, and the i-th
+ *    slot below m that is not kept (ascending) receives K, V, weight and pos
+ *    of the i-th kept slot from m on. No other row moves, so the update is in
+ *    place; the order of slots carries no meaning for 7.
+ *
+ *    weight fp32, pos int32 [B, Hkv, cap]; weight_out, pos_out the same shape
+ *    (they may be weight and pos; if not, slots 0 .. m-1 are written in full).
+ *    keep >= 1; lengths_out int32 [B] = m, not the lengths array itself.
+ *    index       int32 [B, Hkv, min(keep, cap)] or NULL: the source slot of each
+ *                slot below m, -1 after
+ *    Slots from m on keep their contents. Lengths and counts are clamped as in
+ *    7. (DHSA_DEVFLAG_BAD_CACHE), counts to 64; accept needs n_draft.
+ *    workspace: dhsa_cache_evict_workspace_size(B, Hkv, cap) bytes, no initial
+ *    contents needed; calls that share one must not overlap on the GPU.
+ * ------------------------------------------------------------------------- */
+size_t dhsa_cache_evict_workspace_size(int B, int Hkv, int cap);
+int dhsa_cache_evict(void* K, const int64_t* k_strides, void* V, const int64_t* v_strides, const float* weight,
+                     const int32_t* pos, int B, int Hkv, int cap, int head_dim, const int32_t* lengths,
+                     const int32_t* n_draft, const int64_t* accept, int keep, int sinks, int recent,
+                     const int32_t* next_pos, float* weight_out, int32_t* pos_out, int32_t* lengths_out,
+                     int32_t* index, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

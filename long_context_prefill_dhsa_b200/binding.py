@@ -24,6 +24,7 @@ DHSA_OK = 0
 STATUS_NAMES = {0: "DHSA_OK", 1: "DHSA_ERR_INVALID_ARG", 2: "DHSA_ERR_UNSUPPORTED", 3: "DHSA_ERR_CUDA",
                 4: "DHSA_ERR_DEVICE", 5: "DHSA_ERR_WORKSPACE"}
 DEVFLAG_WAIT_TIMEOUT, DEVFLAG_BAD_OFFSETS, DEVFLAG_BAD_SELECTION = 0x1, 0x2, 0x4
+DEVFLAG_BAD_CACHE, DEVFLAG_BAD_TREE = 0x8, 0x10
 
 
 class DHSAError(RuntimeError):
@@ -65,6 +66,14 @@ _SIGNATURES = {
     "dhsa_sparse_attn_tiles_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "dhsa_sparse_attn_fwd_tiles": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _F, _I, _P, _P, _SZ,
                                         _P]),
+    "dhsa_rotary_qkv": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P,
+                             _P, _P, _P, _I, _P, _P]),
+    "dhsa_tree_max_drafts": (_I, []),
+    "dhsa_tree_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "dhsa_tree_attn": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _F, _P, _P, _P, _P, _P, _SZ, _P]),
+    "dhsa_cache_evict_workspace_size": (_SZ, [_I, _I, _I]),
+    "dhsa_cache_evict": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                              _SZ, _P]),
     "dhsa_debug_arm_wait_timeout": (_I, [_I, _c.c_uint64]),
 }
 
@@ -401,6 +410,196 @@ def sparse_attn_fwd_noalloc(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, o
     return out
 
 
+# ----------------------------------------------------------------- rotary positions and the cache
+def _on(t: Optional[torch.Tensor], dtype, shape, name: str, device):
+    """A dense tensor of the call, on the call's device; returns its pointer (None for None)."""
+    if t is None:
+        return None
+    _need(t, dtype, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _rows(t: Optional[torch.Tensor], shape, name: str, device):
+    """A [B, H, rows, 128] bf16 tensor with contiguous rows and any strides:
+    returns its pointer and its strides for the library (None when dense)."""
+    if t is None:
+        return None, None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, expected {device if device.type == 'cuda' else 'a CUDA device'}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
+    return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: torch.Tensor,
+               V: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               start: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+               slots: Optional[torch.Tensor] = None, interleaved: bool = False, transpose: bool = False,
+               factor: float = 1.0, Q_out: Optional[torch.Tensor] = None, K_out: Optional[torch.Tensor] = None,
+               V_out: Optional[torch.Tensor] = None, pos_out: Optional[torch.Tensor] = None):
+    """Rotary positions of Q and K (include/dhsa.h, 6), and K, V (copied) and
+    the positions written into a cache.
+
+    Q [B,Hq,T,128], K and V [B,Hkv,T,128] may be views (e.g. of a
+    [B,T,H,128] projection); any of them may be None. inv_freq: float64
+    [rotary_dim/2]. positions int32 [B,T], or start int32 [B] (start + t), or
+    neither (t). K_out, V_out [B,Hkv,cap,128] receive row t at slots[b] + t
+    (slots None: t); missing outputs are allocated with T rows. Rows
+    t >= n_new[b] are left alone. transpose=True applies the transposed
+    rotation (its gradient). Returns (Q_out, K_out, V_out)."""
+    ref = next((x for x in (Q, K, V) if x is not None), None)
+    if ref is None:
+        raise ValueError("rotary_qkv: Q, K and V are all None")
+    if not isinstance(ref, torch.Tensor) or ref.dim() != 4:
+        raise TypeError("rotary_qkv: expected tensors [B, H, T, 128]")
+    device = ref.device
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return rotary_qkv(Q, K, inv_freq, V, positions, start, n_new, slots, interleaved, transpose, factor,
+                              Q_out, K_out, V_out, pos_out)
+    B, _, T, d = ref.shape
+    Hq = Q.shape[1] if Q is not None else 1
+    kv = K if K is not None else V
+    Hkv = kv.shape[1] if kv is not None else 1
+    q, qs = _rows(Q, (B, Hq, T, d), "Q", device)
+    k, ks = _rows(K, (B, Hkv, T, d), "K", device)
+    v, vs = _rows(V, (B, Hkv, T, d), "V", device)
+    for x, o, name in ((Q, Q_out, "Q_out"), (K, K_out, "K_out"), (V, V_out, "V_out")):
+        if x is None and o is not None:
+            raise ValueError(f"{name}: given without its input")
+    if Q is not None and Q_out is None:
+        Q_out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=device)
+    cap = K_out.shape[2] if K_out is not None else V_out.shape[2] if V_out is not None else T
+    if K is not None and K_out is None:
+        K_out = torch.empty((B, Hkv, cap, d), dtype=torch.bfloat16, device=device)
+    if V is not None and V_out is None:
+        V_out = torch.empty((B, Hkv, cap, d), dtype=torch.bfloat16, device=device)
+    qo = _on(Q_out, torch.bfloat16, (B, Hq, T, d), "Q_out", device)
+    ko, kos = _rows(K_out, (B, Hkv, cap, d), "K_out", device)
+    vo, vos = _rows(V_out, (B, Hkv, cap, d), "V_out", device)
+    if positions is not None and start is not None:
+        raise ValueError("rotary_qkv: positions and start exclude each other")
+    _check(load().dhsa_rotary_qkv(
+        q, qs, k, ks, v, vs, B, Hq, Hkv, T, d, _on(inv_freq, torch.float64, None, "inv_freq", device),
+        2 * inv_freq.numel(), bool(interleaved), bool(transpose), factor,
+        _on(positions, torch.int32, (B, T), "positions", device), _on(start, torch.int32, (B,), "start", device),
+        _on(n_new, torch.int32, (B,), "n_new", device), qo, ko, kos, vo, vos,
+        _on(slots, torch.int32, (B,), "slots", device), cap,
+        _on(pos_out, torch.int32, (B, Hkv, cap), "pos_out", device), _stream_ptr()), "dhsa_rotary_qkv")
+    return Q_out, K_out, V_out
+
+
+def tree_max_drafts() -> int:
+    return load().dhsa_tree_max_drafts()
+
+
+def tree_attn(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lengths: torch.Tensor,
+              parents: Optional[torch.Tensor] = None, n_draft: Optional[torch.Tensor] = None,
+              softmax_scale: Optional[float] = None, weight: Optional[torch.Tensor] = None,
+              weight_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Attention of each sequence's drafted tokens over a cache (include/dhsa.h, 7).
+
+    Q [B,Hq,T,128] dense, T <= 64; caches K, V [B,Hkv,cap,128] (views with
+    contiguous rows will do); lengths int32 [B] cached slots, the drafted
+    tokens' K and V in the slots after them. parents int32 [B,T] is the tree
+    (None: a chain; T = 1 is plain decoding). With `weight` (fp32 [B,Hkv,cap])
+    each slot's attention weight is added to it, into weight_out (None: in
+    place). Returns out (bf16, like Q)."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise TypeError("tree_attn: expected Q [B, Hq, T, 128] and caches [B, Hkv, cap, 128]")
+    device = Q.device
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return tree_attn(Q, K, V, lengths, parents, n_draft, softmax_scale, weight, weight_out, out, lse,
+                             workspace)
+    B, Hq, T, d = Q.shape
+    Hkv, cap = K.shape[1], K.shape[2]
+    q = _on(Q, torch.bfloat16, None, "Q", device)
+    k, ks = _rows(K, (B, Hkv, cap, d), "K", device)
+    v, vs = _rows(V, (B, Hkv, cap, d), "V", device)
+    if weight is None and weight_out is not None:
+        raise ValueError("weight_out: given without weight")
+    if weight is not None and weight_out is None:
+        weight_out = weight
+    if out is None:
+        out = torch.empty_like(Q)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, weight is not None),
+                                dtype=torch.uint8, device=device)
+    _check(lib.dhsa_tree_attn(
+        q, k, ks, v, vs, B, Hq, Hkv, T, cap, d, _on(lengths, torch.int32, (B,), "lengths", device),
+        _on(parents, torch.int32, (B, T), "parents", device), _on(n_draft, torch.int32, (B,), "n_draft", device),
+        1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
+        _on(out, torch.bfloat16, (B, Hq, T, d), "out", device), _on(lse, torch.float32, (B, Hq, T), "lse", device),
+        _on(weight, torch.float32, (B, Hkv, cap), "weight", device),
+        _on(weight_out, torch.float32, (B, Hkv, cap), "weight_out", device),
+        _on(workspace, workspace.dtype, None, "workspace", device), workspace.numel() * workspace.element_size(),
+        _stream_ptr()), "dhsa_tree_attn")
+    return out
+
+
+def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: torch.Tensor, lengths: torch.Tensor,
+                keep: int, next_pos: Optional[torch.Tensor] = None, n_draft: Optional[torch.Tensor] = None,
+                accept: Optional[torch.Tensor] = None, sinks: int = 0, recent: int = 0,
+                weight_out: Optional[torch.Tensor] = None, pos_out: Optional[torch.Tensor] = None,
+                lengths_out: Optional[torch.Tensor] = None, index: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None):
+    """Evict all but `keep` slots of each sequence and kv head, in place, and
+    commit the accepted drafts (include/dhsa.h, 8).
+
+    weight fp32 and pos int32 [B,Hkv,cap] (updated in place unless weight_out
+    and pos_out are given); n_draft int32 [B] drafted slots after `lengths`,
+    of which those with their bit in accept (int64 [B]; None: all) may stay.
+    Slots with pos < sinks or pos >= next_pos - recent rank first. index
+    (int32 [B,Hkv,min(keep,cap)]) receives each slot's source.
+    Returns lengths_out (a new tensor unless given; not `lengths` itself)."""
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise TypeError("cache_evict: expected caches [B, Hkv, cap, 128]")
+    device = K.device
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return cache_evict(K, V, weight, pos, lengths, keep, next_pos, n_draft, accept, sinks, recent, weight_out,
+                               pos_out, lengths_out, index, workspace)
+    B, Hkv, cap, d = K.shape
+    k, ks = _rows(K, (B, Hkv, cap, d), "K", device)
+    v, vs = _rows(V, (B, Hkv, cap, d), "V", device)
+    if weight_out is None:
+        weight_out = weight
+    if pos_out is None:
+        pos_out = pos
+    if lengths_out is None:
+        lengths_out = torch.empty_like(lengths)
+    keep = min(int(keep), 0x7fffffff)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.dhsa_cache_evict_workspace_size(B, Hkv, cap), dtype=torch.uint8, device=device)
+    _check(lib.dhsa_cache_evict(
+        k, ks, v, vs, _on(weight, torch.float32, (B, Hkv, cap), "weight", device),
+        _on(pos, torch.int32, (B, Hkv, cap), "pos", device), B, Hkv, cap, d,
+        _on(lengths, torch.int32, (B,), "lengths", device), _on(n_draft, torch.int32, (B,), "n_draft", device),
+        _on(accept, torch.int64, (B,), "accept", device), keep, int(sinks), int(recent),
+        _on(next_pos, torch.int32, (B,), "next_pos", device),
+        _on(weight_out, torch.float32, (B, Hkv, cap), "weight_out", device),
+        _on(pos_out, torch.int32, (B, Hkv, cap), "pos_out", device),
+        _on(lengths_out, torch.int32, (B,), "lengths_out", device),
+        _on(index, torch.int32, (B, Hkv, min(keep, cap)), "index", device),
+        _on(workspace, workspace.dtype, None, "workspace", device), workspace.numel() * workspace.element_size(),
+        _stream_ptr()), "dhsa_cache_evict")
+    return lengths_out
+
+
 # ----------------------------------------------------------------- whole layer
 class DHSAPrefill:
     """The five calls of one DHSA prefill layer with buffers allocated once.
@@ -416,11 +615,16 @@ class DHSAPrefill:
     launch (route_fused; top-k rule only). Under the top-k rule the selection
     writes the CSR itself (chunk_score_topk_csr); `csr_from_selection=False`
     runs the separate CSR build instead (the same results).
+    With `inv_freq` (float64 [rotary_dim/2], see rotary_qkv) run() takes Q and
+    K before their rotary positions and rotates them first, at positions
+    0 .. L-1, into its own Qr and Kr; Q and K may then be views. Without it
+    they are taken as rotated.
     """
 
     def __init__(self, B: int, Hq: int, Hkv: int, L: int, off: torch.Tensor, n_chunks: torch.Tensor, k: int,
                  device="cuda", softmax_scale: Optional[float] = None, budget=None, recent: int = 0,
-                 short_tiles: int = 0, fused_routing: bool = False, csr_from_selection: bool = True):
+                 short_tiles: int = 0, fused_routing: bool = False, csr_from_selection: bool = True,
+                 inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, rotary_factor: float = 1.0):
         lib = load()
         self.B, self.Hq, self.Hkv, self.L, self.k = B, Hq, Hkv, L, k
         self.short_tiles = short_tiles
@@ -447,6 +651,18 @@ class DHSAPrefill:
         self.ws_attn = torch.empty(max(lib.dhsa_sparse_attn_tiles_workspace_size(B, Hq, L, nmax, short_tiles), 1),
                                    dtype=torch.uint8, device=dev)
         self.O = torch.empty((B, Hq, L, 128), dtype=torch.bfloat16, device=dev)
+        self.inv_freq, self.interleaved, self.rotary_factor = inv_freq, interleaved, rotary_factor
+        if inv_freq is not None:
+            self.Qr = torch.empty((B, Hq, L, 128), dtype=torch.bfloat16, device=dev)
+            self.Kr = torch.empty((B, Hkv, L, 128), dtype=torch.bfloat16, device=dev)
+
+    def rotate(self, Q, K):
+        """Q and K at their rotary positions (as they are without inv_freq)."""
+        if self.inv_freq is None:
+            return Q, K
+        rotary_qkv(Q, K, self.inv_freq, interleaved=self.interleaved, factor=self.rotary_factor, Q_out=self.Qr,
+                   K_out=self.Kr)
+        return self.Qr, self.Kr
 
     def routing(self, Q, K):
         if self.fused_routing:
@@ -473,6 +689,7 @@ class DHSAPrefill:
                                self.scale, out=self.O, workspace=self.ws_attn, short_tiles=self.short_tiles)
 
     def run(self, Q, K, V):
+        Q, K = self.rotate(Q, K)
         self.routing(Q, K)
         return self.attention(Q, K, V)
 
@@ -519,8 +736,9 @@ class HostStreamedPrefill:
         if self.n >= 2:
             self.s_comp.wait_event(self.e_out[b])      # layer n-2's O has left this buffer
         with torch.cuda.stream(self.s_comp):
-            lay.routing(self.Qd[b], self.Kd[b])
-            sparse_attn_fwd(self.Qd[b], self.Kd[b], self.Vd[b], lay.off, lay.n_chunks, lay.row_ptr, lay.col_idx,
+            Q, K = lay.rotate(self.Qd[b], self.Kd[b])
+            lay.routing(Q, K)
+            sparse_attn_fwd(Q, K, self.Vd[b], lay.off, lay.n_chunks, lay.row_ptr, lay.col_idx,
                             lay.cost, lay.scale, out=self.Od[b], workspace=lay.ws_attn)
             self.e_comp[b].record(self.s_comp)
         self.s_out.wait_event(self.e_comp[b])

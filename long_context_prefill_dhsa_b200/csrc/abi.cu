@@ -2,6 +2,7 @@
 // stage launchers. Every check happens before anything is enqueued.
 #include <cstring>
 
+#include "cache.cuh"
 #include "common.cuh"
 
 namespace dhsa {
@@ -33,6 +34,24 @@ int launch_sparse_attn(const void* Q, const void* K, const void* V, int B, int H
                        const int32_t* off, const int32_t* n_chunks, int Nmax, const int32_t* row_ptr,
                        const int32_t* col_idx, float softmax_scale, int policy, void* O, void* ws,
                        unsigned int* status, cudaStream_t stream);
+int launch_rotary(const void* Q, const RowStrides& qs, const void* K, const RowStrides& ks, const void* V,
+                  const RowStrides& vs, int B, int Hq, int Hkv, int T, const double* inv_freq, int rotary_dim,
+                  bool interleaved, bool transpose, float factor, const int32_t* positions, const int32_t* start,
+                  const int32_t* n_new, void* Qo, void* Ko, const RowStrides& kos, void* Vo, const RowStrides& vos,
+                  const int32_t* slots, int cap, int32_t* pos_out, unsigned int* status, cudaStream_t stream);
+int tree_max_drafts();
+int tree_max_group();
+size_t tree_ws_bytes(int B, int Hq, int Hkv, int T, int cap, bool want_weight);
+int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const void* V, const RowStrides& vs, int B,
+                     int Hq, int Hkv, int T, int cap, const int32_t* lengths, const int32_t* parents,
+                     const int32_t* n_draft, float softmax_scale, void* O, float* lse, const float* weight,
+                     float* weight_out, void* ws, unsigned int* status, cudaStream_t stream);
+size_t evict_ws_bytes(int B, int Hkv, int cap);
+int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, const float* weight,
+                 const int32_t* pos, int B, int Hkv, int cap, const int32_t* lengths, const int32_t* n_draft,
+                 const int64_t* accept, int keep, int sinks, int recent, const int32_t* next_pos, float* weight_out,
+                 int32_t* pos_out, int32_t* lengths_out, int32_t* index, void* ws, unsigned int* status,
+                 cudaStream_t stream);
 size_t noalloc_scratch_bytes();
 int noalloc_scratch_ptr(void** out);
 
@@ -124,7 +143,7 @@ const char* dhsa_status_string(int status) {
 
 int dhsa_last_cuda_error(void) { return t_last_cuda_error; }
 
-int dhsa_version(void) { return 300; }   // 0.3.0: wait-timeout test hook; offsets clamped by pooling and the work list
+int dhsa_version(void) { return 400; }   // 0.4.0: rotary positions, attention of drafted tokens over a cache, cache eviction
 
 int dhsa_check_device_status(void* stream, uint32_t* device_flags) {
   if (device_flags) *device_flags = 0;
@@ -366,6 +385,109 @@ int dhsa_sparse_attn_fwd_noalloc(const void* Q, const void* K, const void* V, in
   if ((st = noalloc_scratch_ptr(&scratch)) != DHSA_OK) return st;
   return launch_sparse_attn(Q, K, V, B, Hq, Hkv, L, off, n_chunks, Nmax, row_ptr, col_idx, softmax_scale, 0, O,
                             scratch, status, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+// a cache's [B, Hkv, cap, 128] extent: its rows are counted in int32
+int check_cache(int B, int Hkv, int cap, int head_dim) {
+  if (B <= 0 || Hkv <= 0 || cap <= 0) return DHSA_ERR_INVALID_ARG;
+  if ((long long)B * Hkv * cap > 0x7fffffffLL) return DHSA_ERR_INVALID_ARG;
+  if (head_dim != kHeadDim) return DHSA_ERR_UNSUPPORTED;
+  return DHSA_OK;
+}
+}  // namespace
+
+int dhsa_rotary_qkv(const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
+                    const int64_t* v_strides, int B, int Hq, int Hkv, int T, int head_dim, const double* inv_freq,
+                    int rotary_dim, int interleaved, int transpose, float factor, const int32_t* positions,
+                    const int32_t* start, const int32_t* n_new, void* Q_out, void* K_out, const int64_t* ko_strides,
+                    void* V_out, const int64_t* vo_strides, const int32_t* slots, int cap, int32_t* pos_out,
+                    void* stream) {
+  int st = check_cache(B, Hkv, cap, head_dim);
+  if (st != DHSA_OK) return st;
+  if (Hq <= 0 || T <= 0 || (long long)B * Hq * T > 0x7fffffffLL || (long long)B * Hkv * T > 0x7fffffffLL)
+    return DHSA_ERR_INVALID_ARG;
+  if (Hq + 2LL * Hkv > 65535) return DHSA_ERR_INVALID_ARG;   // grid rows
+  if ((!Q && !K && !V) || !Q != !Q_out || !K != !K_out || !V != !V_out || (pos_out && !K)) return DHSA_ERR_INVALID_ARG;
+  if (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) || rotary_dim < 16 || rotary_dim > kHeadDim ||
+      rotary_dim % 16 != 0)
+    return DHSA_ERR_INVALID_ARG;
+  if (!slots && cap < T) return DHSA_ERR_INVALID_ARG;
+  if (!(factor - factor == 0.f)) return DHSA_ERR_INVALID_ARG;   // not finite
+  const void* ptrs[6] = {Q, K, V, Q_out, K_out, V_out};
+  for (const void* x : ptrs)
+    if (!aligned16(x)) return DHSA_ERR_INVALID_ARG;
+  RowStrides qs, ks, vs, kos, vos;
+  if (!read_strides(q_strides, B, Hq, T, false, &qs) || !read_strides(k_strides, B, Hkv, T, false, &ks) ||
+      !read_strides(v_strides, B, Hkv, T, false, &vs) || !read_strides(ko_strides, B, Hkv, cap, true, &kos) ||
+      !read_strides(vo_strides, B, Hkv, cap, true, &vos))
+    return DHSA_ERR_INVALID_ARG;
+  if ((st = check_device_sm100()) != DHSA_OK) return st;
+  unsigned int* status = device_status_ptr();
+  if (!status) return DHSA_ERR_CUDA;
+  return launch_rotary(Q, qs, K, ks, V, vs, B, Hq, Hkv, T, inv_freq, rotary_dim, interleaved != 0, transpose != 0,
+                       factor, positions, start, n_new, Q_out, K_out, kos, V_out, vos, slots, cap, pos_out, status,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int dhsa_tree_max_drafts(void) { return tree_max_drafts(); }
+
+size_t dhsa_tree_attn_workspace_size(int B, int Hq, int Hkv, int T, int cap, int want_weight) {
+  if (check_cache(B, Hkv, cap, kHeadDim) != DHSA_OK || Hq <= 0 || Hq % Hkv != 0 || T <= 0 || T > tree_max_drafts())
+    return 0;
+  return tree_ws_bytes(B, Hq, Hkv, T, cap, want_weight != 0);
+}
+
+int dhsa_tree_attn(const void* Q, const void* K, const int64_t* k_strides, const void* V, const int64_t* v_strides,
+                   int B, int Hq, int Hkv, int T, int cap, int head_dim, const int32_t* lengths,
+                   const int32_t* parents, const int32_t* n_draft, float softmax_scale, void* O, float* lse,
+                   const float* weight, float* weight_out, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_cache(B, Hkv, cap, head_dim);
+  if (st != DHSA_OK) return st;
+  if (!Q || !K || !V || !lengths || !O || !weight != !weight_out) return DHSA_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % Hkv != 0 || T <= 0) return DHSA_ERR_INVALID_ARG;
+  if ((long long)B * Hq * T > 0x7fffffffLL) return DHSA_ERR_INVALID_ARG;
+  if (T > tree_max_drafts() || Hq / Hkv > tree_max_group()) return DHSA_ERR_UNSUPPORTED;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return DHSA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale - softmax_scale != 0.f) return DHSA_ERR_INVALID_ARG;
+  RowStrides ks, vs;
+  if (!read_strides(k_strides, B, Hkv, cap, true, &ks) || !read_strides(v_strides, B, Hkv, cap, true, &vs))
+    return DHSA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < tree_ws_bytes(B, Hq, Hkv, T, cap, weight != nullptr) || !aligned16(workspace))
+    return DHSA_ERR_WORKSPACE;
+  if ((st = check_device_sm100()) != DHSA_OK) return st;
+  unsigned int* status = device_status_ptr();
+  if (!status) return DHSA_ERR_CUDA;
+  return launch_tree_attn(Q, K, ks, V, vs, B, Hq, Hkv, T, cap, lengths, parents, n_draft, softmax_scale, O, lse,
+                          weight, weight_out, workspace, status, static_cast<cudaStream_t>(stream));
+}
+
+size_t dhsa_cache_evict_workspace_size(int B, int Hkv, int cap) {
+  if (check_cache(B, Hkv, cap, kHeadDim) != DHSA_OK) return 0;
+  return evict_ws_bytes(B, Hkv, cap);
+}
+
+int dhsa_cache_evict(void* K, const int64_t* k_strides, void* V, const int64_t* v_strides, const float* weight,
+                     const int32_t* pos, int B, int Hkv, int cap, int head_dim, const int32_t* lengths,
+                     const int32_t* n_draft, const int64_t* accept, int keep, int sinks, int recent,
+                     const int32_t* next_pos, float* weight_out, int32_t* pos_out, int32_t* lengths_out,
+                     int32_t* index, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_cache(B, Hkv, cap, head_dim);
+  if (st != DHSA_OK) return st;
+  if (!K || !V || !weight || !pos || !lengths || !weight_out || !pos_out || !lengths_out) return DHSA_ERR_INVALID_ARG;
+  if (lengths_out == lengths) return DHSA_ERR_INVALID_ARG;   // the heads of a sequence read lengths at their own time
+  if (keep <= 0 || sinks < 0 || recent < 0 || (recent > 0 && !next_pos) || (accept && !n_draft))
+    return DHSA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || (reinterpret_cast<uintptr_t>(accept) & 7u)) return DHSA_ERR_INVALID_ARG;
+  RowStrides ks, vs;
+  if (!read_strides(k_strides, B, Hkv, cap, true, &ks) || !read_strides(v_strides, B, Hkv, cap, true, &vs))
+    return DHSA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < evict_ws_bytes(B, Hkv, cap) || !aligned16(workspace)) return DHSA_ERR_WORKSPACE;
+  if ((st = check_device_sm100()) != DHSA_OK) return st;
+  unsigned int* status = device_status_ptr();
+  if (!status) return DHSA_ERR_CUDA;
+  return launch_evict(K, ks, V, vs, weight, pos, B, Hkv, cap, lengths, n_draft, accept, keep, sinks, recent, next_pos,
+                      weight_out, pos_out, lengths_out, index, workspace, status, static_cast<cudaStream_t>(stream));
 }
 
 int dhsa_debug_arm_wait_timeout(int mode, uint64_t limit_ns) {

@@ -1,0 +1,48 @@
+// Shared by the calls on a key/value cache (rotary.cu, tree_attn.cu, evict.cu):
+// row strides, and the clamped view of a sequence's lengths.
+#pragma once
+#include "common.cuh"
+
+namespace dhsa {
+
+// strides in elements of a [B, H, rows, 128] tensor with contiguous rows
+struct RowStrides {
+  long long b, h, r;
+};
+
+inline RowStrides dense_strides(int H, int rows) {
+  return RowStrides{(long long)H * rows * kHeadDim, (long long)rows * kHeadDim, kHeadDim};
+}
+
+// s: three host int64 or null (dense). False if a stride cannot be used: not
+// a multiple of 8 elements, negative, or (distinct_rows) shorter than a row
+// along a dimension with more than one entry.
+inline bool read_strides(const int64_t* s, int B, int H, int rows, bool distinct_rows, RowStrides* out) {
+  *out = dense_strides(H, rows);
+  if (!s) return true;
+  const int n[3] = {B, H, rows};
+  long long* o[3] = {&out->b, &out->h, &out->r};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;   // never multiplied by anything but 0
+    if (s[i] < 0 || s[i] % 8 != 0 || (distinct_rows && s[i] < kHeadDim)) return false;
+    *o[i] = s[i];
+  }
+  return true;
+}
+
+// A sequence's cached slots and drafted tokens, clamped into the cache.
+struct SeqLen {
+  int len, draft;
+  bool bad;
+};
+__device__ __forceinline__ SeqLen seq_len(const int32_t* lengths, const int32_t* n_draft, int no_draft, int b,
+                                          int max_draft, int cap) {
+  const int l = lengths[b], d = n_draft ? n_draft[b] : no_draft;
+  SeqLen s;
+  s.len = min(max(l, 0), cap);
+  s.draft = min(min(max(d, 0), max_draft), cap - s.len);
+  s.bad = s.len != l || s.draft != d;
+  return s;
+}
+
+}  // namespace dhsa

@@ -10,4 +10,5 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA device (B200, sm_100a)")
+    config.addinivalue_line("markers", "expects_flag: leaves device status flags for itself to read")
     config.addinivalue_line("markers", "slow: CPU test that takes more than a few seconds")
