@@ -2,133 +2,589 @@
 //
 // Token t of sequence b sees the cached slots s < len, itself and its
 // ancestors in the drafted tree; O = softmax(scale q k) v over them.
-#include "cache.cuh"
+//
+// The G query heads of a kv head and their T tokens read the same keys, so
+// their G*T rows (contiguous in Q) are one matrix operand, and each key and
+// value is read from HBM once: 512 bytes per slot against 512 FLOP per slot
+// and row. Up to about 250 rows HBM is the bound, above them the tensor cores
+// and the exponentials.
+//
+// sm_100a design
+// --------------
+// * Work: the 128-slot key tiles of all (sequence, kv head, query block) items
+//   are one line, cut into equal shares, one per CTA of a persistent grid; a
+//   share covers the end of one item, some whole ones and the start of
+//   another. Lengths are read on the device, so ragged batches balance
+//   without host help. Each piece of an item leaves an unnormalised O with
+//   its running maximum and sum, and a second kernel joins an item's pieces.
+// * Two softmax streams per CTA, each with its own S and O in TMEM (4 x 128
+//   columns) and its own four warps. With up to 128 rows they take the even
+//   and the odd key tiles of the same query tile; with more they take two
+//   query tiles over the same key tiles. While one stream does its
+//   exponentials the tensor core works for the other.
+// * Warp 0 streams K and V tiles (TMA, 32 KB each) into one ring; warp 1
+//   issues S = Q K^T (both operands in shared memory) and O += P V (P from
+//   TMEM, over the S it came from); warps 4 to 11 are the streams' softmax.
+//   A single issuer keeps the tensor operations of a stream in order: S(i+1)
+//   complete means P(i) V(i) complete.
+// * Query row r sits in TMEM lane 32 (r mod 4) + r / 4, so that few rows (one
+//   token: G of them) spread over all four lane quarters, and the shape
+//   16x256b gives each row to four threads.
+// * P is rounded to bf16 for the tensor core, as V is bf16 and both operands
+//   share a type; the row sum adds the fp32 values.
+// * Slots past the last one can hold anything: their scores are replaced, and
+//   their V rows are zeroed in shared memory (0 x NaN would be NaN).
+// * Every wait is bounded; a timeout raises DHSA_DEVFLAG_WAIT_TIMEOUT, and the
+//   CTA drains its copies and MMAs, frees its TMEM and exits.
+#include "tree.cuh"
 
 namespace dhsa {
+
+int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream);
+
 namespace {
 
-constexpr int kMaxDrafts = 64;   // one bit of a 64-bit word each
-constexpr int kMaxGroup = 64;    // query heads of one kv head
+constexpr int kThreads = 384;
+constexpr int kSmemTiles = 7;    // 32 KB each: query tiles (1 or 2), the rest is the K/V ring
 
-struct TreeParams {
-  const __nv_bfloat16 *Q, *K, *V;
-  RowStrides ks, vs;
-  const int32_t *lengths, *parents, *n_draft;
-  __nv_bfloat16* O;
-  float *lse, *lse_ws;
-  const float* weight;
-  float* weight_out;
-  int B, Hq, Hkv, G, T, cap;
-  float scale_log2;
-  unsigned int* status;
+struct TreeMaps {
+  CUtensorMap k, v;
 };
 
-// drafted tokens that token t sees, one bit each
-__device__ __forceinline__ uint64_t sees(const int32_t* parents, int t, unsigned int* status) {
-  if (!parents) return t >= 63 ? ~0ull : (2ull << t) - 1;
-  uint64_t m = 0;
-  for (int a = t; a >= 0;) {
-    m |= 1ull << a;
-    const int up = parents[a];
-    if (up < -1 || up >= a) {
-      raise_device_flag(status, DHSA_DEVFLAG_BAD_TREE);
-      break;
-    }
-    a = up;
-  }
-  return m;
-}
+// shared memory after the tiles
+enum {
+  B_FULL = 0,                   // ring stage holds its tile
+  B_EMPTY = B_FULL + kSmemTiles - 1,
+  B_QREADY = B_EMPTY + kSmemTiles - 1,
+  B_SFULL,                      // per stream: S complete
+  B_PREADY = B_SFULL + 2,       // per stream: P written
+  B_OFINAL = B_PREADY + 2,      // every MMA of the piece complete
+  B_FINAL,
+  B_TEARDOWN,
+  B_COUNT
+};
+constexpr uint32_t OFF_BAR = kSmemTiles * kTileBytes;
+constexpr uint32_t OFF_LINE = OFF_BAR + 8 * ((B_COUNT + 1) & ~1);
+constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
+constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
+constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;   // slack for aligning the base
+static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(Line) % 8 == 0, "alignment");
 
-__global__ void __launch_bounds__(256) tree_rows_kernel(const TreeParams p) {
-  __shared__ float sm[8], sl[8], so[8][kHeadDim];
-  const int t = blockIdx.x % p.T, hq = blockIdx.x / p.T % p.Hq, b = blockIdx.x / p.T / p.Hq;
+constexpr int W_PRODUCER = 0, W_MMA = 1, W_SOFTMAX0 = 4;
+
+template <int NQT>   // query tiles per CTA
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ TreeMaps maps,
+                                                                const TreeParams p) {
+  constexpr int NST = kSmemTiles - NQT;      // ring stages
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t ring = sbase + NQT * kTileBytes;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+  Line* line = reinterpret_cast<Line*>(smem + OFF_LINE);
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-  if (s.bad && threadIdx.x == 0) raise_device_flag(p.status, DHSA_DEVFLAG_BAD_CACHE);
-  if (t >= s.draft) return;
-  const uint64_t mask = sees(p.parents ? p.parents + b * p.T : nullptr, t, p.status);
-  const long long row = ((long long)b * p.Hq + hq) * p.T + t;
-  const int h = hq / p.G;
-  const __nv_bfloat16* kb = p.K + b * p.ks.b + h * p.ks.h + lane * 4;
-  const __nv_bfloat16* vb = p.V + b * p.vs.b + h * p.vs.h + lane * 4;
-  float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0;
-  for (int i = 0; i < 4; ++i) q[i] = __bfloat162float(p.Q[row * kHeadDim + lane * 4 + i]) * p.scale_log2;
-  for (int j = warp; j < s.len + s.draft; j += 8) {
-    if (j >= s.len && !((mask >> (j - s.len)) & 1)) continue;
-    float d = 0;
-    for (int i = 0; i < 4; ++i) d += q[i] * __bfloat162float(kb[j * p.ks.r + i]);
-    for (int o2 = 16; o2 > 0; o2 >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o2);
-    const float n = fmaxf(m, d), f = exp2f(m - n), e = exp2f(d - n);
-    l = l * f + e;
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * __bfloat162float(vb[j * p.vs.r + i]);
-    m = n;
+
+  if (warp == W_PRODUCER) {
+    if (lane == 0) {
+      *abort_flag = 0;
+      for (int s = 0; s < NST; ++s) {
+        mbar_init(bar(B_FULL + s), 1);
+        mbar_init(bar(B_EMPTY + s), 1);
+      }
+      mbar_init(bar(B_QREADY), 8);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(bar(B_SFULL + s), 1);
+        mbar_init(bar(B_PREADY + s), 4);
+      }
+      mbar_init(bar(B_OFINAL), 1);
+      mbar_init(bar(B_FINAL), 1);
+      mbar_init(bar(B_TEARDOWN), kThreads / 32 - 1);
+      fence_mbar_init();
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+    }
+  } else if (warp == W_MMA) {
+    tmem_alloc(sbase + OFF_TMEMPTR, kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
+    const Line L = find_share(p, blockIdx.x, lane);
+    if (lane == 0) *line = L;
+  } else if (warp == 3 && blockIdx.x == 0) {
+    bool bad = false;
+    for (int b = lane; b < p.B; b += 32) bad |= seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap).bad;
+    if (bad) raise_device_flag(p.status, DHSA_DEVFLAG_BAD_CACHE);
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  for (int i = 0; i < 4; ++i) so[warp][lane * 4 + i] = o[i];
+  tc_fence_before();
   __syncthreads();
-  float M = -INFINITY, L = 0, x = 0;
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < 8; ++w) {
-    const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - M);
-    L += sl[w] * f;
-    if (threadIdx.x < kHeadDim) x += so[w][threadIdx.x] * f;
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR);
+  const Waits wait{abort_flag, p.status};
+  Pieces walk{line->start, line->end, line->base, line->b};
+  Piece w{};
+
+  if (warp == W_PRODUCER) {
+    if (lane == 0) {
+      uint32_t g = 0;     // tiles loaded
+      bool ok = true;
+      auto load = [&](const CUtensorMap* m, int tile) {
+        const uint32_t st = g % NST;
+        if (g >= NST && !wait(bar(B_EMPTY + st), (g / NST - 1) & 1)) return false;
+        const uint32_t dst = ring + st * kTileBytes;
+        mbar_arrive_expect_tx(bar(B_FULL + st), kTileBytes);
+        tma_load_4d(dst, m, bar(B_FULL + st), 0, tile * BN, w.h, w.b);
+        tma_load_4d(dst + kHalfBytes, m, bar(B_FULL + st), 64, tile * BN, w.h, w.b);
+        ++g;
+        return true;
+      };
+      while (ok && walk.next(p, &w)) {
+        // the order in which the issuer uses them: with one query tile
+        // K0 K1 V0 K2 V1 ..., with two K0 V0 K1 V1 ...
+        constexpr int kAhead = NQT == 1 ? 2 : 1;
+        for (int i = 0; ok && i < kAhead && i < w.n; ++i) ok = load(&maps.k, w.t0 + i);
+        for (int i = 0; ok && i < w.n; ++i) {
+          ok = load(&maps.v, w.t0 + i);
+          if (ok && i + kAhead < w.n) ok = load(&maps.k, w.t0 + i + kAhead);
+        }
+      }
+      // copies in flight must land before the CTA ends
+      for (uint32_t q = g > NST ? g - NST : 0; q < g; ++q) mbar_wait(bar(B_FULL + q % NST), (q / NST) & 1, kWaitLimitNs);
+    }
+  } else if (warp == W_MMA) {
+    if (lane == 0) {
+      const uint32_t idesc_qk = idesc_bf16_f32(BM, BN, false), idesc_pv = idesc_bf16_f32(BM, kHeadDim, true);
+      uint32_t g = 0, n_p[2] = {0, 0}, n_piece = 0;
+      auto qk = [&](int s, uint32_t stage) {      // S[s] = Q K^T
+        const uint32_t qa = sbase + (NQT == 2 ? s * kTileBytes : 0), ka = ring + stage * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t o = (k >> 2) * kHalfBytes + (k & 3) * 32;
+          mma_ss(tmem + s * 128, smem_desc_sw128(qa + o, 16, 1024), smem_desc_sw128(ka + o, 16, 1024), idesc_qk,
+                 k > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(B_SFULL + s));
+      };
+      auto pv = [&](int s, uint32_t stage, bool first) {      // O[s] += P V
+        const uint32_t va = ring + stage * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, smem_desc_sw128(va + k * 2048, kHalfBytes, 1024),
+                 idesc_pv, (!first || k > 0) ? 1u : 0u);
+      };
+      auto arrived = [&](uint32_t q) {
+        const bool ok = wait(bar(B_FULL + q % NST), (q / NST) & 1);
+        tc_fence_after();
+        return ok;
+      };
+      auto p_ready = [&](int s) {
+        const bool ok = wait(bar(B_PREADY + s), n_p[s]++ & 1);
+        tc_fence_after();
+        return ok;
+      };
+      bool ok = true;
+      while (ok && walk.next(p, &w)) {
+        if (!wait(bar(B_QREADY), n_piece & 1)) break;
+        tc_fence_after();
+        if (NQT == 1) {
+          for (int i = 0; ok && i < 2 && i < w.n; ++i) {
+            if (!(ok = arrived(g))) break;
+            qk(i, g % NST);
+            mma_commit(bar(B_EMPTY + g++ % NST));
+          }
+          for (int i = 0; ok && i < w.n; ++i) {
+            if (!(ok = p_ready(i & 1) && arrived(g))) break;
+            pv(i & 1, g % NST, i < 2);
+            mma_commit(bar(B_EMPTY + g++ % NST));
+            if (i + 2 < w.n) {
+              if (!(ok = arrived(g))) break;
+              qk(i & 1, g % NST);
+              mma_commit(bar(B_EMPTY + g++ % NST));
+            }
+          }
+        } else {
+          if (!(ok = arrived(g))) break;
+          qk(0, g % NST);
+          qk(1, g % NST);
+          mma_commit(bar(B_EMPTY + g++ % NST));
+          for (int i = 0; ok && i < w.n; ++i) {
+            const bool more = i + 1 < w.n;
+            const uint32_t gv = g++, gk = more ? g++ : 0;
+            if (!(ok = p_ready(0) && arrived(gv))) break;
+            pv(0, gv % NST, i == 0);
+            if (more) {
+              if (!(ok = arrived(gk))) break;
+              qk(0, gk % NST);
+            }
+            if (!(ok = p_ready(1))) break;
+            pv(1, gv % NST, i == 0);
+            mma_commit(bar(B_EMPTY + gv % NST));
+            if (more) {
+              qk(1, gk % NST);
+              mma_commit(bar(B_EMPTY + gk % NST));
+            }
+          }
+        }
+        if (!ok) break;
+        mma_commit(bar(B_OFINAL));
+        ++n_piece;
+      }
+      mma_commit(bar(B_FINAL));
+      mbar_wait(bar(B_FINAL), 0, kWaitLimitNs);
+    }
+  } else if (warp >= W_SOFTMAX0) {
+    const int stream = (warp - W_SOFTMAX0) >> 2, quarter = warp & 3;
+    const int cq = lane & 3;
+    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + stream * 128;
+    const uint32_t tO = tS + 256;
+    const float c = p.scale_log2, raise = 8.f / c;
+    uint32_t g = 0, n_s = 0, n_piece = 0;   // ring tiles and S tiles used so far, pieces
+    bool ok = true;
+    while (ok && walk.next(p, &w)) {
+      // ---- the query tiles: eight warps, 16 (32) shared-memory rows each
+      const __nv_bfloat16* q_head = p.Q + ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T * kHeadDim;
+      const int row0 = w.block * (NQT == 2 ? 2 * BM : BM);      // first row of the block
+#pragma unroll
+      for (int it = 0; it < 8 * NQT; ++it) {
+        const int at = (warp - W_SOFTMAX0) * 16 * NQT + it * 2 + (lane >> 4);   // shared-memory row, over both tiles
+        const int L = at & 127, tile = at >> 7, ch = lane & 15;
+        const int r = row0 + tile * BM + 4 * (L & 31) + (L >> 5);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < p.rows) v = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
+        *reinterpret_cast<uint4*>(smem + tile * kTileBytes + (ch >> 3) * kHalfBytes + L * 128 +
+                                  (((ch & 7) ^ (L & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_QREADY));
+
+      // ---- this thread's rows: lane quarter, two halves of 16 lanes, rows A (lane / 4) and B (+ 8)
+      const int srow0 = row0 + (NQT == 2 ? stream * BM : 0);    // first row of this stream's tile
+      const int srows = min(p.rows - srow0, BM);                // valid rows of it (can be <= 0)
+      const int in_q = srows > quarter ? (srows - quarter + 3) >> 2 : 0;   // of this quarter
+      const int groups = (in_q + 7) >> 3;                       // of eight rows
+      uint64_t see[4];
+      const int tail0 = w.len / BN;                             // first tile with drafted or empty slots
+      const bool tail = w.t0 + w.n > tail0;
+      if (tail) {
+        const Sees sv = tree_sees(p, w.b, w.draft, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = srow0 + 4 * (8 * k + (lane >> 2)) + quarter;
+          see[k] = sv.of(r % p.T);
+        }
+      }
+      float m[4], l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+      }
+      constexpr int step = NQT == 1 ? 2 : 1;
+      for (int i = NQT == 1 ? stream : 0; i < w.n; i += step) {
+        if (!(ok = wait(bar(B_SFULL + stream), n_s & 1))) break;
+        tc_fence_after();
+        const int k0 = (w.t0 + i) * BN;             // first slot of the tile
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (groups <= 2 * hf) break;
+          const bool both = groups > 2 * hf + 1;
+          const uint32_t tSh = tS + ((uint32_t)(16 * hf) << 16), tOh = tO + ((uint32_t)(16 * hf) << 16);
+          // s[4j + e]: row A, slot k0 + 8j + 2cq + e; s[4j + 2 + e]: row B
+          uint32_t s[64];
+          tmem_ld_16x256b_x8(tSh, *reinterpret_cast<uint32_t(*)[32]>(s));
+          tmem_ld_16x256b_x8(tSh + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          tmem_wait_ld();
+          if (k0 + BN > w.len) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int d = k0 + 8 * j + 2 * cq + e - w.len;      // drafted token of the slot
+                const uint32_t sh = (uint32_t)d & 63u;
+                if (d >= 0 && (d >= 64 || !((see[2 * hf] >> sh) & 1))) s[4 * j + e] = __float_as_uint(-INFINITY);
+                if (d >= 0 && (d >= 64 || !((see[2 * hf + 1] >> sh) & 1)))
+                  s[4 * j + 2 + e] = __float_as_uint(-INFINITY);
+              }
+          }
+          auto S = [&](int e) { return __uint_as_float(s[e]); };
+          float xA = fmaxf(S(0), S(1)), xB = fmaxf(S(2), S(3));
+#pragma unroll
+          for (int j = 1; j < 16; ++j) {
+            xA = fmaxf(xA, fmaxf(S(4 * j), S(4 * j + 1)));
+            xB = fmaxf(xB, fmaxf(S(4 * j + 2), S(4 * j + 3)));
+          }
+          xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, 1));
+          xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, 1));
+          xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, 2));
+          xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, 2));
+          float &mA = m[2 * hf], &mB = m[2 * hf + 1];
+          // the maximum is raised, and O rescaled, only when it grows by more
+          // than 2^8: O / l is exact all the same, and p stays below 2^8
+          const bool rA = xA > mA + raise, rB = both && xB > mB + raise;
+          if (__any_sync(0xffffffffu, rA || rB)) {
+            const float fA = rA ? fast_exp2((mA - xA) * c) : 1.f, fB = rB ? fast_exp2((mB - xB) * c) : 1.f;
+            if (rA) {
+              mA = xA;
+              l[2 * hf] *= fA;
+            }
+            if (rB) {
+              mB = xB;
+              l[2 * hf + 1] *= fB;
+            }
+            if (i >= step) {      // S complete implies the stream's last P V complete
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t o[16];
+                tmem_ld_16x256b_x4(tOh + 32 * q, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  o[4 * j] = __float_as_uint(__uint_as_float(o[4 * j]) * fA);
+                  o[4 * j + 1] = __float_as_uint(__uint_as_float(o[4 * j + 1]) * fA);
+                  o[4 * j + 2] = __float_as_uint(__uint_as_float(o[4 * j + 2]) * fB);
+                  o[4 * j + 3] = __float_as_uint(__uint_as_float(o[4 * j + 3]) * fB);
+                }
+                tmem_st_16x256b_x4(tOh + 32 * q, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          // The difference is taken before the scale: scores near the maximum
+          // keep their distance to it exactly, however large they are. A row
+          // that has seen nothing yet keeps m = -inf: its p are 0.
+          const float nA = mA == -INFINITY ? 0.f : -mA, nB = mB == -INFINITY ? 0.f : -mB;
+          float sA = 0.f, sB = 0.f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int j = 8 * q + u;
+              const float a0 = fast_exp2((S(4 * j) + nA) * c), a1 = fast_exp2((S(4 * j + 1) + nA) * c);
+              sA += a0 + a1;
+              pk[2 * u] = pack_bf16x2(a0, a1);
+            }
+            if (both) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const int j = 8 * q + u;
+                const float b0 = fast_exp2((S(4 * j + 2) + nB) * c), b1 = fast_exp2((S(4 * j + 3) + nB) * c);
+                sB += b0 + b1;
+                pk[2 * u + 1] = pack_bf16x2(b0, b1);
+              }
+            } else {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) pk[2 * u + 1] = 0u;
+            }
+            tmem_st_16x128b_x8(tSh + 32 * q, pk);
+          }
+          l[2 * hf] += sA;
+          l[2 * hf + 1] += sB;
+        }
+        // V rows past the last slot: zero them before the product reads them
+        const int slots = w.len + w.draft;
+        if (k0 + BN > slots && (NQT == 1 || stream == 0)) {
+          const uint32_t q = g + 2 * w.n - 1;      // the item's last tile is the piece's last load
+          if (!(ok = wait(bar(B_FULL + q % NST), (q / NST) & 1))) break;
+          unsigned char* v = smem + (NQT + q % NST) * kTileBytes;
+          for (int x = (slots - k0) * 16 + quarter * 32 + lane; x < BN * 16; x += 128)
+            *reinterpret_cast<uint4*>(v + (x & 1) * kHalfBytes + (x >> 1) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PREADY + stream));
+        ++n_s;
+      }
+      if (!ok) break;
+      g += 2 * w.n;
+      // ---- the piece's partial result
+      if (!(ok = wait(bar(B_OFINAL), n_piece & 1))) break;
+      ++n_piece;
+      tc_fence_after();
+      const bool used = NQT == 2 || w.n > stream;     // a stream without tiles has no O
+      const long long slot = ((long long)blockIdx.x + w.item) * 2 + stream;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (groups <= 2 * hf) break;
+        const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
+        float lA = l[2 * hf], lB = l[2 * hf + 1];
+        lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+        lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+        lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+        lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+        const int ra = 4 * (16 * hf + (lane >> 2)) + quarter, rb = ra + 32;     // rows within the tile
+        if (cq == 0) {
+          if (ra < srows) p.part_ml[slot * p.row_cap + ra] = make_float2(m[2 * hf], lA);
+          if (rb < srows) p.part_ml[slot * p.row_cap + rb] = make_float2(m[2 * hf + 1], lB);
+        }
+        if (used) {
+          float* oa = p.part_o + (slot * p.row_cap + ra) * kHeadDim + 2 * cq;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[16];
+            tmem_ld_16x256b_x4(tOh + 32 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (ra < srows)
+                *reinterpret_cast<uint2*>(oa + 32 * q + 8 * j) = make_uint2(o[4 * j], o[4 * j + 1]);
+              if (rb < srows)
+                *reinterpret_cast<uint2*>(oa + 32 * kHeadDim + 32 * q + 8 * j) = make_uint2(o[4 * j + 2], o[4 * j + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    }
   }
-  if (threadIdx.x < kHeadDim) p.O[row * kHeadDim + threadIdx.x] = __float2bfloat16(x / L);
+
+  // Every warp reports and exits; warp 1 frees TMEM once all have.
+  __syncwarp();
+  tc_fence_before();
+  if (warp != W_MMA) {
+    if (lane == 0) mbar_arrive(bar(B_TEARDOWN));
+    return;
+  }
+  mbar_wait(bar(B_TEARDOWN), 0, kWaitLimitNs);
+  __syncwarp();
+  tc_fence_after();
+  tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the pieces of one row: O = sum_i f_i O_i / sum_i f_i l_i, f_i =
+// exp(scale (m_i - M)).
+// One block of 128 threads per row, one thread per element.
+__global__ void __launch_bounds__(kHeadDim) tree_combine_kernel(const TreeParams p) {
+  __shared__ float f[2 * kMaxGrid];
+  __shared__ long long at[2 * kMaxGrid];
+  __shared__ int count;
+  __shared__ float top, sum;
+  const int r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
+  const int b = bh / p.Hkv, h = bh % p.Hkv, t = r % p.T;
+  const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
+  if (t >= s.draft) return;
+  const int wide = p.rows > BM ? 2 : 1;              // query tiles of a block
+  const int block = r / (wide * BM), tile = r / BM % wide, tr = r % BM;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    long long sum_all = 0, sum_before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int n = b0 + lane < p.B ? key_tiles(p, b0 + lane) : 0;
+      sum_all += __reduce_add_sync(0xffffffffu, n);
+      sum_before += __reduce_add_sync(0xffffffffu, b0 + lane < b ? n : 0);
+    }
+    const long long per = (long long)p.Hkv * p.blocks, total = per * sum_all;
+    const int nt = (s.len + s.draft + BN - 1) / BN;
+    const long long a = per * sum_before + ((long long)h * p.blocks + block) * nt, e = a + nt;
+    const int item = bh * p.blocks + block;
+    // the CTAs whose shares [total c / grid, total (c + 1) / grid) meet [a, e)
+    const int c0 = (int)(((a + 1) * p.grid + total - 1) / total) - 1, c1 = (int)((e * p.grid + total - 1) / total) - 1;
+    int n = 0;
+    float mx = -INFINITY;
+    for (int x0 = c0 * 2; x0 <= c1 * 2 + 1; x0 += 32) {
+      const int x = x0 + lane, c = x >> 1, stream = x & 1;
+      bool has = c <= c1 && total * c / p.grid < total * (c + 1) / p.grid && (wide == 1 || stream == tile);
+      const long long slot = ((long long)(c + item) * 2 + stream) * p.row_cap + tr;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (has) ml = p.part_ml[slot];
+      has = has && ml.x != -INFINITY;
+      const uint32_t v = __ballot_sync(0xffffffffu, has);
+      if (has) {
+        const int q = n + __popc(v & ((1u << lane) - 1));
+        f[q] = ml.x;
+        at[q] = slot;
+      }
+      n += __popc(v);
+      mx = fmaxf(mx, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    __syncwarp();
+    float l = 0.f;
+    for (int q = lane; q < n; q += 32) {
+      const float k = fast_exp2((f[q] - mx) * p.scale_log2);
+      l += k * p.part_ml[at[q]].y;
+      f[q] = k;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      count = n;
+      top = mx;
+      sum = l;
+    }
+  }
+  __syncthreads();
+  float o = 0.f;
+  const int n = count;
+#pragma unroll 4
+  for (int q = 0; q < n; ++q) o += f[q] * p.part_o[at[q] * kHeadDim + threadIdx.x];
+  const long long row = (long long)bh * p.rows + r;
+  p.O[row * kHeadDim + threadIdx.x] = __float2bfloat16(n ? o / sum : 0.f);
   if (threadIdx.x == 0) {
-    const float lse2 = M + log2f(L);
-    if (p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
-    if (p.lse_ws) p.lse_ws[row] = lse2;
+    if (p.lse) p.lse[row] = n ? top * p.scale + logf(sum) : -INFINITY;
+    if (p.row_stat) p.row_stat[row] = make_float2(top, 1.f / sum);
   }
 }
 
-// one warp per slot
-__global__ void __launch_bounds__(256) tree_weight_kernel(const TreeParams p) {
-  const long long idx = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (idx >= (long long)p.B * p.Hkv * p.cap) return;
-  const int slot = (int)(idx % p.cap), h = (int)(idx / p.cap % p.Hkv), b = (int)(idx / p.cap / p.Hkv);
-  const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-  if (slot >= s.len + s.draft) return;
-  float k[4], sum = 0;
-  for (int i = 0; i < 4; ++i)
-    k[i] = __bfloat162float(p.K[b * p.ks.b + h * p.ks.h + slot * p.ks.r + lane * 4 + i]) * p.scale_log2;
-  for (int t = 0; t < s.draft; ++t) {
-    if (slot >= s.len && !((sees(p.parents ? p.parents + b * p.T : nullptr, t, p.status) >> (slot - s.len)) & 1)) continue;
-    for (int g = 0; g < p.G; ++g) {
-      const long long row = ((long long)b * p.Hq + h * p.G + g) * p.T + t;
-      float d = 0;
-      for (int i = 0; i < 4; ++i) d += k[i] * __bfloat162float(p.Q[row * kHeadDim + lane * 4 + i]);
-      for (int o2 = 16; o2 > 0; o2 >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o2);
-      sum += exp2f(d - p.lse_ws[row]);
-    }
-  }
-  if (lane == 0) p.weight_out[idx] = (slot < s.len ? p.weight[idx] : 0.f) + sum;
+struct Plan {
+  int rows, wide, blocks, row_cap;
+  size_t o_bytes, ml_bytes, stat_bytes;
+};
+Plan make_plan(int B, int Hq, int Hkv, int T, bool want_weight) {
+  Plan q;
+  q.rows = Hq / Hkv * T;
+  q.wide = q.rows > BM ? 2 : 1;
+  q.blocks = ceil_div(q.rows, q.wide * BM);
+  q.row_cap = q.rows < BM ? q.rows : BM;
+  const size_t pieces = (size_t)B * Hkv * q.blocks + kMaxGrid;
+  q.o_bytes = pieces * 2 * q.row_cap * kHeadDim * sizeof(float);   // a multiple of 512
+  q.ml_bytes = (pieces * 2 * q.row_cap * sizeof(float2) + 255) / 256 * 256;
+  q.stat_bytes = want_weight ? sizeof(float2) * (size_t)B * Hq * T : 0;
+  return q;
 }
 
 }  // namespace
 
 int tree_max_drafts() { return kMaxDrafts; }
 int tree_max_group() { return kMaxGroup; }
+
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
-  return 256 + sizeof(float) * (size_t)B * Hq * T;
+  const Plan q = make_plan(B, Hq, Hkv, T, want_weight);
+  return q.o_bytes + q.ml_bytes + q.stat_bytes;
 }
 
 int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const void* V, const RowStrides& vs, int B,
                      int Hq, int Hkv, int T, int cap, const int32_t* lengths, const int32_t* parents,
                      const int32_t* n_draft, float softmax_scale, void* O, float* lse, const float* weight,
                      float* weight_out, void* ws, unsigned int* status, cudaStream_t stream) {
+  const Plan q = make_plan(B, Hq, Hkv, T, weight_out != nullptr);
+  EncodeTiledFn enc = tmap_encode_fn();
+  if (!enc) return cuda_status(cudaErrorNotSupported);
+  TreeMaps maps;
+  if (!make_cache_map(enc, &maps.k, K, ks, B, Hkv, cap) || !make_cache_map(enc, &maps.v, V, vs, B, Hkv, cap))
+    return DHSA_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  auto* kernel = q.wide == 2 ? tree_attn_kernel<2> : tree_attn_kernel<1>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemAlloc);
+  if (e != cudaSuccess) return cuda_status(e);
+
   TreeParams p;
   p.Q = static_cast<const __nv_bfloat16*>(Q);
-  p.K = static_cast<const __nv_bfloat16*>(K);
-  p.V = static_cast<const __nv_bfloat16*>(V);
-  p.ks = ks;
-  p.vs = vs;
   p.lengths = lengths;
   p.parents = parents;
   p.n_draft = n_draft;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.lse = lse;
-  p.lse_ws = weight_out ? static_cast<float*>(ws) : nullptr;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + q.o_bytes);
+  p.row_stat = weight_out ? reinterpret_cast<float2*>(static_cast<char*>(ws) + q.o_bytes + q.ml_bytes) : nullptr;
   p.weight = weight;
   p.weight_out = weight_out;
   p.B = B;
@@ -137,12 +593,28 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.G = Hq / Hkv;
   p.T = T;
   p.cap = cap;
+  p.rows = q.rows;
+  p.blocks = q.blocks;
+  p.row_cap = q.row_cap;
+  p.every = false;
+  const long long most = (long long)B * Hkv * q.blocks * ceil_div(cap, BN);   // tiles at full lengths
+  p.grid = sms < kMaxGrid ? sms : kMaxGrid;
+  if (most < p.grid) p.grid = (int)most;
+  p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = status;
-  tree_rows_kernel<<<B * Hq * T, 256, 0, stream>>>(p);
-  if (weight_out)
-    tree_weight_kernel<<<(unsigned)(((long long)B * Hkv * cap + 7) / 8), 256, 0, stream>>>(p);
-  return launch_status();
+  kernel<<<p.grid, kThreads, kSmemAlloc, stream>>>(maps, p);
+  tree_combine_kernel<<<(unsigned)((long long)B * Hkv * q.rows), kHeadDim, 0, stream>>>(p);
+  int st = launch_status();
+  if (st == DHSA_OK && weight_out) {
+    p.every = true;                   // weights without new tokens are passed on
+    p.blocks = 1;                     // one walk over the keys for all rows of a head
+    p.grid = sms < kMaxGrid ? sms : kMaxGrid;
+    const long long tiles = (long long)B * Hkv * ceil_div(cap, BN);
+    if (tiles < p.grid) p.grid = (int)tiles;
+    st = launch_tree_weight(maps.k, p, stream);
+  }
+  return st;
 }
 
 }  // namespace dhsa
