@@ -64,7 +64,8 @@ enum {
   B_COUNT
 };
 constexpr uint32_t OFF_BAR = kSmemTiles * kTileBytes;
-constexpr uint32_t OFF_LINE = OFF_BAR + 8 * ((B_COUNT + 1) & ~1);
+constexpr uint32_t OFF_SEE = OFF_BAR + 8 * ((B_COUNT + 1) & ~1);   // drafted tokens that each drafted token sees
+constexpr uint32_t OFF_LINE = OFF_SEE + kMaxDrafts * 8;
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;   // slack for aligning the base
@@ -239,21 +240,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + stream * 128;
     const uint32_t tO = tS + 256;
     const float c = p.scale_log2, raise = 8.f / c;
+    const uint64_t c2 = pk2(c, c);
+    // written by every softmax warp with the same values
+    uint64_t* see = reinterpret_cast<uint64_t*>(smem + OFF_SEE);
     uint32_t g = 0, n_s = 0, n_piece = 0;   // ring tiles and S tiles used so far, pieces
     bool ok = true;
     while (ok && walk.next(p, &w)) {
       // ---- the query tiles: eight warps, 16 (32) shared-memory rows each
       const __nv_bfloat16* q_head = p.Q + ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T * kHeadDim;
       const int row0 = w.block * (NQT == 2 ? 2 * BM : BM);      // first row of the block
+      const int ch = lane & 15;
 #pragma unroll
-      for (int it = 0; it < 8 * NQT; ++it) {
-        const int at = (warp - W_SOFTMAX0) * 16 * NQT + it * 2 + (lane >> 4);   // shared-memory row, over both tiles
-        const int L = at & 127, tile = at >> 7, ch = lane & 15;
-        const int r = row0 + tile * BM + 4 * (L & 31) + (L >> 5);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < p.rows) v = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
-        *reinterpret_cast<uint4*>(smem + tile * kTileBytes + (ch >> 3) * kHalfBytes + L * 128 +
-                                  (((ch & 7) ^ (L & 7)) << 4)) = v;
+      for (int part = 0; part < NQT; ++part) {      // eight loads in flight
+        uint4 v[8];
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int L = (warp - W_SOFTMAX0) * 16 + it * 2 + (lane >> 4);     // shared-memory row of the tile
+          const int r = row0 + part * BM + 4 * (L & 31) + (L >> 5);
+          v[it] = make_uint4(0, 0, 0, 0);
+          if (r < p.rows) v[it] = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
+        }
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int L = (warp - W_SOFTMAX0) * 16 + it * 2 + (lane >> 4);
+          *reinterpret_cast<uint4*>(smem + part * kTileBytes + (ch >> 3) * kHalfBytes + L * 128 +
+                                    (((ch & 7) ^ (L & 7)) << 4)) = v[it];
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -264,31 +276,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const int srows = min(p.rows - srow0, BM);                // valid rows of it (can be <= 0)
       const int in_q = srows > quarter ? (srows - quarter + 3) >> 2 : 0;   // of this quarter
       const int groups = (in_q + 7) >> 3;                       // of eight rows
-      uint64_t see[4];
       const int tail0 = w.len / BN;                             // first tile with drafted or empty slots
       const bool tail = w.t0 + w.n > tail0;
       if (tail) {
         const Sees sv = tree_sees(p, w.b, w.draft, lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = srow0 + 4 * (8 * k + (lane >> 2)) + quarter;
-          see[k] = sv.of(r % p.T);
-        }
+        see[lane] = sv.m0;
+        see[lane + 32] = sv.m1;
+        __syncwarp();
       }
-      float m[4], l[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m[k] = -INFINITY;
-        l[k] = 0.f;
-      }
+      // running maximum (raw scores) and sum of this thread's rows: A and B of the first half, then of the second
+      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
       constexpr int step = NQT == 1 ? 2 : 1;
       for (int i = NQT == 1 ? stream : 0; i < w.n; i += step) {
         if (!(ok = wait(bar(B_SFULL + stream), n_s & 1))) break;
         tc_fence_after();
         const int k0 = (w.t0 + i) * BN;             // first slot of the tile
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (groups <= 2 * hf) break;
+        // one or two halves of 16 lanes; after each, the halves' states change places
+        const int halves = groups > 2 ? 2 : groups > 0 ? 1 : 0;
+#pragma unroll 1
+        for (int hf = 0; hf < halves; ++hf) {
           const bool both = groups > 2 * hf + 1;
           const uint32_t tSh = tS + ((uint32_t)(16 * hf) << 16), tOh = tO + ((uint32_t)(16 * hf) << 16);
           // s[4j + e]: row A, slot k0 + 8j + 2cq + e; s[4j + 2 + e]: row B
@@ -297,44 +303,47 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           tmem_ld_16x256b_x8(tSh + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
           tmem_wait_ld();
           if (k0 + BN > w.len) {
+            const int rA = srow0 + 4 * (16 * hf + (lane >> 2)) + quarter;
+            const uint64_t seeA = see[rA % p.T], seeB = see[(rA + 32) % p.T];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int d = k0 + 8 * j + 2 * cq + e - w.len;      // drafted token of the slot
                 const uint32_t sh = (uint32_t)d & 63u;
-                if (d >= 0 && (d >= 64 || !((see[2 * hf] >> sh) & 1))) s[4 * j + e] = __float_as_uint(-INFINITY);
-                if (d >= 0 && (d >= 64 || !((see[2 * hf + 1] >> sh) & 1)))
-                  s[4 * j + 2 + e] = __float_as_uint(-INFINITY);
+                if (d >= 0 && (d >= 64 || !((seeA >> sh) & 1))) s[4 * j + e] = __float_as_uint(-INFINITY);
+                if (d >= 0 && (d >= 64 || !((seeB >> sh) & 1))) s[4 * j + 2 + e] = __float_as_uint(-INFINITY);
               }
           }
           auto S = [&](int e) { return __uint_as_float(s[e]); };
-          float xA = fmaxf(S(0), S(1)), xB = fmaxf(S(2), S(3));
+          float a0 = fmaxf(S(0), S(1)), a1 = fmaxf(S(4), S(5)), b0 = fmaxf(S(2), S(3)), b1 = fmaxf(S(6), S(7));
 #pragma unroll
-          for (int j = 1; j < 16; ++j) {
-            xA = fmaxf(xA, fmaxf(S(4 * j), S(4 * j + 1)));
-            xB = fmaxf(xB, fmaxf(S(4 * j + 2), S(4 * j + 3)));
+          for (int j = 2; j < 16; j += 2) {
+            a0 = max3(a0, S(4 * j), S(4 * j + 1));
+            a1 = max3(a1, S(4 * j + 4), S(4 * j + 5));
+            b0 = max3(b0, S(4 * j + 2), S(4 * j + 3));
+            b1 = max3(b1, S(4 * j + 6), S(4 * j + 7));
           }
+          float xA = fmaxf(a0, a1), xB = fmaxf(b0, b1);
           xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, 1));
           xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, 1));
           xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, 2));
           xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, 2));
-          float &mA = m[2 * hf], &mB = m[2 * hf + 1];
           // the maximum is raised, and O rescaled, only when it grows by more
           // than 2^8: O / l is exact all the same, and p stays below 2^8
-          const bool rA = xA > mA + raise, rB = both && xB > mB + raise;
+          const bool rA = xA > m0 + raise, rB = both && xB > m1 + raise;
           if (__any_sync(0xffffffffu, rA || rB)) {
-            const float fA = rA ? fast_exp2((mA - xA) * c) : 1.f, fB = rB ? fast_exp2((mB - xB) * c) : 1.f;
+            const float fA = rA ? fast_exp2((m0 - xA) * c) : 1.f, fB = rB ? fast_exp2((m1 - xB) * c) : 1.f;
             if (rA) {
-              mA = xA;
-              l[2 * hf] *= fA;
+              m0 = xA;
+              l0 *= fA;
             }
             if (rB) {
-              mB = xB;
-              l[2 * hf + 1] *= fB;
+              m1 = xB;
+              l1 *= fB;
             }
             if (i >= step) {      // S complete implies the stream's last P V complete
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < 4; ++q) {
                 uint32_t o[16];
                 tmem_ld_16x256b_x4(tOh + 32 * q, o);
@@ -354,34 +363,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           // The difference is taken before the scale: scores near the maximum
           // keep their distance to it exactly, however large they are. A row
           // that has seen nothing yet keeps m = -inf: its p are 0.
-          const float nA = mA == -INFINITY ? 0.f : -mA, nB = mB == -INFINITY ? 0.f : -mB;
-          float sA = 0.f, sB = 0.f;
+          const float nA = m0 == -INFINITY ? 0.f : -m0, nB = m1 == -INFINITY ? 0.f : -m1;
+          const uint64_t nA2 = pk2(nA, nA), nB2 = pk2(nB, nB);
+          uint64_t sA = 0ull, sB = 0ull;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
+            // pk[2u]: row A, pk[2u + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
             uint32_t pk[16];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const int j = 8 * q + u;
-              const float a0 = fast_exp2((S(4 * j) + nA) * c), a1 = fast_exp2((S(4 * j + 1) + nA) * c);
-              sA += a0 + a1;
-              pk[2 * u] = pack_bf16x2(a0, a1);
+              float x0, x1;
+              unpk2(mul2(add2(pk2(S(4 * j), S(4 * j + 1)), nA2), c2), x0, x1);
+              x0 = fast_exp2(x0);
+              x1 = fast_exp2(x1);
+              sA = add2(sA, pk2(x0, x1));
+              pk[2 * u] = pack_bf16x2(x0, x1);
+              pk[2 * u + 1] = 0u;
             }
             if (both) {
 #pragma unroll
               for (int u = 0; u < 8; ++u) {
                 const int j = 8 * q + u;
-                const float b0 = fast_exp2((S(4 * j + 2) + nB) * c), b1 = fast_exp2((S(4 * j + 3) + nB) * c);
-                sB += b0 + b1;
-                pk[2 * u + 1] = pack_bf16x2(b0, b1);
+                float x0, x1;
+                unpk2(mul2(add2(pk2(S(4 * j + 2), S(4 * j + 3)), nB2), c2), x0, x1);
+                x0 = fast_exp2(x0);
+                x1 = fast_exp2(x1);
+                sB = add2(sB, pk2(x0, x1));
+                pk[2 * u + 1] = pack_bf16x2(x0, x1);
               }
-            } else {
-#pragma unroll
-              for (int u = 0; u < 8; ++u) pk[2 * u + 1] = 0u;
             }
             tmem_st_16x128b_x8(tSh + 32 * q, pk);
           }
-          l[2 * hf] += sA;
-          l[2 * hf + 1] += sB;
+          float x0, x1;
+          unpk2(sA, x0, x1);
+          l0 += x0 + x1;
+          unpk2(sB, x0, x1);
+          l1 += x0 + x1;
+          if (halves == 2) {
+            float y;
+            y = m0; m0 = m2; m2 = y;
+            y = m1; m1 = m3; m3 = y;
+            y = l0; l0 = l2; l2 = y;
+            y = l1; l1 = l3; l3 = y;
+          }
         }
         // V rows past the last slot: zero them before the product reads them
         const int slots = w.len + w.draft;
@@ -411,15 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       for (int hf = 0; hf < 2; ++hf) {
         if (groups <= 2 * hf) break;
         const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
-        float lA = l[2 * hf], lB = l[2 * hf + 1];
+        float lA = hf ? l2 : l0, lB = hf ? l3 : l1;
         lA += __shfl_xor_sync(0xffffffffu, lA, 1);
         lB += __shfl_xor_sync(0xffffffffu, lB, 1);
         lA += __shfl_xor_sync(0xffffffffu, lA, 2);
         lB += __shfl_xor_sync(0xffffffffu, lB, 2);
         const int ra = 4 * (16 * hf + (lane >> 2)) + quarter, rb = ra + 32;     // rows within the tile
         if (cq == 0) {
-          if (ra < srows) p.part_ml[slot * p.row_cap + ra] = make_float2(m[2 * hf], lA);
-          if (rb < srows) p.part_ml[slot * p.row_cap + rb] = make_float2(m[2 * hf + 1], lB);
+          if (ra < srows) p.part_ml[slot * p.row_cap + ra] = make_float2(hf ? m2 : m0, lA);
+          if (rb < srows) p.part_ml[slot * p.row_cap + rb] = make_float2(hf ? m3 : m1, lB);
         }
         if (used) {
           float* oa = p.part_o + (slot * p.row_cap + ra) * kHeadDim + 2 * cq;

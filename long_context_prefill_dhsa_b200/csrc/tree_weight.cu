@@ -43,30 +43,6 @@ constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 
-__device__ __forceinline__ uint64_t pk2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpk2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                   const TreeParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -185,15 +161,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         // the Q operand and the row statistics: 32 rows per warp. Rows past
         // the end and of missing tokens are zeros with weight 0.
         const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock), n_pad = (n_rows + 15) & ~15;
-        for (int it = 0; it < 16; ++it) {
-          const int at = (warp - 4) * 32 + it * 2 + (lane >> 4), ch = lane & 15;
-          if (at >= n_pad) break;        // n_pad is even: both half-warps leave together
-          const int r = rb * kRowBlock + at;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (at < n_rows && r % p.T < w.draft)
-            v = *reinterpret_cast<const uint4*>(p.Q + (row_base + r) * kHeadDim + ch * 8);
-          *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * kQHalfBytes + at * 128 +
-                                    (((ch & 7) ^ (at & 7)) << 4)) = v;
+        const int ch = lane & 15;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {       // eight loads in flight
+          uint4 v[8];
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int at = (warp - 4) * 32 + half * 16 + it * 2 + (lane >> 4), r = rb * kRowBlock + at;
+            v[it] = make_uint4(0, 0, 0, 0);
+            if (at < n_rows && r % p.T < w.draft)
+              v[it] = *reinterpret_cast<const uint4*>(p.Q + (row_base + r) * kHeadDim + ch * 8);
+          }
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int at = (warp - 4) * 32 + half * 16 + it * 2 + (lane >> 4);
+            if (at < n_pad)
+              *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * kQHalfBytes + at * 128 +
+                                        (((ch & 7) ^ (at & 7)) << 4)) = v[it];
+          }
         }
         {
           const int at = (warp - 4) * 32 + lane, r = rb * kRowBlock + at;
