@@ -31,13 +31,13 @@ inline bool read_strides(const int64_t* s, int B, int H, int rows, bool distinct
   return true;
 }
 
-// TMA map of a cache: boxes of 64 columns x 128 slots of one head, 128-byte
-// swizzle; slots past the capacity read as zeros.
+// TMA map of a cache: boxes of 64 columns x box_rows slots of one head,
+// 128-byte swizzle; slots past the capacity read as zeros.
 inline bool make_cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, const RowStrides& s, int B, int Hkv,
-                           int cap) {
+                           int cap, int box_rows) {
   const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)cap, (cuuint64_t)Hkv, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)s.r * 2, (cuuint64_t)s.h * 2, (cuuint64_t)s.b * 2};
-  const cuuint32_t box[4] = {64u, 128u, 1u, 1u};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 1u, 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

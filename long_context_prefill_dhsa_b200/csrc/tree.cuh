@@ -21,6 +21,7 @@ struct TreeParams {
   int rows;                 // G * T
   int blocks;               // query blocks of a kv head that walk the keys
   int row_cap;              // rows of a stream's partial
+  int tile;                 // slots of a key tile
   int grid;                 // CTAs that share the key tiles
   bool every;               // sequences without drafted tokens are walked too
   float scale, scale_log2;
@@ -35,15 +36,11 @@ constexpr int kMaxDrafts = 64;   // one bit of a 64-bit word each
 constexpr int kMaxGroup = 64;    // query heads of one kv head
 constexpr int kMaxGrid = 160;    // CTAs (one per SM) the workspace is sized for
 
-constexpr int BM = 128;          // query rows per tile
-constexpr int BN = 128;          // slots per key tile
-constexpr uint32_t kHalfBytes = 128 * 128;   // 128 rows x 64 bf16, 128-byte swizzle
-constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr uint32_t kTmemCols = 512;
 
 // key tiles of each item of sequence b
 __device__ __forceinline__ int key_tiles(const TreeParams& p, const SeqLen& s) {
-  return s.draft > 0 || p.every ? (s.len + s.draft + BN - 1) / BN : 0;
+  return s.draft > 0 || p.every ? (s.len + s.draft + p.tile - 1) / p.tile : 0;
 }
 __device__ __forceinline__ int key_tiles(const TreeParams& p, int b) {
   return key_tiles(p, seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap));

@@ -21,12 +21,12 @@
 //   columns) and its own four warps. With up to 128 rows they take the even
 //   and the odd key tiles of the same query tile; with more they take two
 //   query tiles over the same key tiles. While one stream does its
-//   exponentials the tensor core works for the other.
+//   exponentials the tensor core works for the other, and each half of P
+//   goes to the tensor core while the softmax does the other half.
 // * Warp 0 streams K and V tiles (TMA, 32 KB each) into one ring; warp 1
 //   issues S = Q K^T (both operands in shared memory) and O += P V (P from
 //   TMEM, over the S it came from); warps 4 to 11 are the streams' softmax.
-//   A single issuer keeps the tensor operations of a stream in order: S(i+1)
-//   complete means P(i) V(i) complete.
+//   A single issuer keeps the tensor operations in order.
 // * Query row r sits in TMEM lane 32 (r mod 4) + r / 4, so that few rows (one
 //   token: G of them) spread over all four lane quarters, and the shape
 //   16x256b gives each row to four threads.
@@ -40,12 +40,21 @@
 
 namespace dhsa {
 
+int tree_weight_tile();
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream);
 
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kSmemTiles = 7;    // 32 KB each: query tiles (1 or 2), the rest is the K/V ring
+constexpr int BM = 128;          // query rows per tile
+constexpr int BN = 128;          // slots per key tile
+constexpr uint32_t kHalfBytes = BM * 128;    // 128 query rows x 64 bf16, 128-byte swizzle
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;
+constexpr uint32_t kKvHalfBytes = BN * 128;
+constexpr uint32_t kKvBytes = 2 * kKvHalfBytes;
+constexpr float kRaise = 20.f;   // powers of two by which a score may pass its row's reference
+constexpr uint32_t kSmemData = 224 * 1024;   // query tiles (one or two of 32 KB), the rest is the ring of K and V tiles
+constexpr int kMaxStages = (kSmemData - kTileBytes) / kKvBytes;
 
 struct TreeMaps {
   CUtensorMap k, v;
@@ -54,16 +63,17 @@ struct TreeMaps {
 // shared memory after the tiles
 enum {
   B_FULL = 0,                   // ring stage holds its tile
-  B_EMPTY = B_FULL + kSmemTiles - 1,
-  B_QREADY = B_EMPTY + kSmemTiles - 1,
+  B_EMPTY = B_FULL + kMaxStages,
+  B_QREADY = B_EMPTY + kMaxStages,
   B_SFULL,                      // per stream: S complete
-  B_PREADY = B_SFULL + 2,       // per stream: P written
-  B_OFINAL = B_PREADY + 2,      // every MMA of the piece complete
+  B_PREADY = B_SFULL + 2,       // [stream][half]: P of 64 slots written
+  B_PVHALF = B_PREADY + 4,      // per stream: P V of a tile's first half complete
+  B_OFINAL = B_PVHALF + 2,      // every MMA of the piece complete
   B_FINAL,
   B_TEARDOWN,
   B_COUNT
 };
-constexpr uint32_t OFF_BAR = kSmemTiles * kTileBytes;
+constexpr uint32_t OFF_BAR = kSmemData;
 constexpr uint32_t OFF_SEE = OFF_BAR + 8 * ((B_COUNT + 1) & ~1);   // drafted tokens that each drafted token sees
 constexpr uint32_t OFF_LINE = OFF_SEE + kMaxDrafts * 8;
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
@@ -77,7 +87,8 @@ constexpr int W_PRODUCER = 0, W_MMA = 1, W_SOFTMAX0 = 4;
 template <int NQT>   // query tiles per CTA
 __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ TreeMaps maps,
                                                                 const TreeParams p) {
-  constexpr int NST = kSmemTiles - NQT;      // ring stages
+  constexpr int NST = (kSmemData - NQT * kTileBytes) / kKvBytes;   // ring stages
+  constexpr int kAhead = 2 / NQT;   // tiles whose scores are computed ahead: one S for each of two streams
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -96,9 +107,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         mbar_init(bar(B_EMPTY + s), 1);
       }
       mbar_init(bar(B_QREADY), 8);
+      for (int s = 0; s < 4; ++s) mbar_init(bar(B_PREADY + s), 4);
       for (int s = 0; s < 2; ++s) {
         mbar_init(bar(B_SFULL + s), 1);
-        mbar_init(bar(B_PREADY + s), 4);
+        mbar_init(bar(B_PVHALF + s), 1);
       }
       mbar_init(bar(B_OFINAL), 1);
       mbar_init(bar(B_FINAL), 1);
@@ -133,17 +145,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       auto load = [&](const CUtensorMap* m, int tile) {
         const uint32_t st = g % NST;
         if (g >= NST && !wait(bar(B_EMPTY + st), (g / NST - 1) & 1)) return false;
-        const uint32_t dst = ring + st * kTileBytes;
-        mbar_arrive_expect_tx(bar(B_FULL + st), kTileBytes);
+        const uint32_t dst = ring + st * kKvBytes;
+        mbar_arrive_expect_tx(bar(B_FULL + st), kKvBytes);
         tma_load_4d(dst, m, bar(B_FULL + st), 0, tile * BN, w.h, w.b);
-        tma_load_4d(dst + kHalfBytes, m, bar(B_FULL + st), 64, tile * BN, w.h, w.b);
+        tma_load_4d(dst + kKvHalfBytes, m, bar(B_FULL + st), 64, tile * BN, w.h, w.b);
         ++g;
         return true;
       };
       while (ok && walk.next(p, &w)) {
-        // the order in which the issuer uses them: with one query tile
-        // K0 K1 V0 K2 V1 ..., with two K0 V0 K1 V1 ...
-        constexpr int kAhead = NQT == 1 ? 2 : 1;
+        // the order in which the issuer uses them: K tiles kAhead before V tiles
         for (int i = 0; ok && i < kAhead && i < w.n; ++i) ok = load(&maps.k, w.t0 + i);
         for (int i = 0; ok && i < w.n; ++i) {
           ok = load(&maps.v, w.t0 + i);
@@ -156,70 +166,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   } else if (warp == W_MMA) {
     if (lane == 0) {
       const uint32_t idesc_qk = idesc_bf16_f32(BM, BN, false), idesc_pv = idesc_bf16_f32(BM, kHeadDim, true);
-      uint32_t g = 0, n_p[2] = {0, 0}, n_piece = 0;
-      auto qk = [&](int s, uint32_t stage) {      // S[s] = Q K^T
-        const uint32_t qa = sbase + (NQT == 2 ? s * kTileBytes : 0), ka = ring + stage * kTileBytes;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t o = (k >> 2) * kHalfBytes + (k & 3) * 32;
-          mma_ss(tmem + s * 128, smem_desc_sw128(qa + o, 16, 1024), smem_desc_sw128(ka + o, 16, 1024), idesc_qk,
-                 k > 0 ? 1u : 0u);
-        }
-        mma_commit(bar(B_SFULL + s));
-      };
-      auto pv = [&](int s, uint32_t stage, bool first) {      // O[s] += P V
-        const uint32_t va = ring + stage * kTileBytes;
+      uint32_t g = 0, n_piece = 0, p_phase = 0;    // p_phase: parity of P's barriers, a bit for each stream
+      auto qk = [&](int s, uint32_t stage) {      // S = Q K^T
+        const uint32_t qa = sbase + (NQT == 2 ? s * kTileBytes : 0), ka = ring + stage * kKvBytes;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, smem_desc_sw128(va + k * 2048, kHalfBytes, 1024),
-                 idesc_pv, (!first || k > 0) ? 1u : 0u);
+          mma_ss(tmem + s * 128, smem_desc_sw128(qa + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024),
+                 smem_desc_sw128(ka + (k >> 2) * kKvHalfBytes + (k & 3) * 32, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
+        mma_commit(bar(B_SFULL + s));
       };
       auto arrived = [&](uint32_t q) {
         const bool ok = wait(bar(B_FULL + q % NST), (q / NST) & 1);
         tc_fence_after();
         return ok;
       };
-      auto p_ready = [&](int s) {
-        const bool ok = wait(bar(B_PREADY + s), n_p[s]++ & 1);
-        tc_fence_after();
-        return ok;
+      auto pv = [&](int s, uint32_t q, bool first) {      // O += P V, each half as soon as its P is there
+        const uint32_t va = ring + (q % NST) * kKvBytes;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(bar(B_PREADY + 2 * s + half), (p_phase >> s) & 1)) return false;
+          if (half == 0 && !wait(bar(B_FULL + q % NST), (q / NST) & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k)
+            mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, smem_desc_sw128(va + k * 2048, kKvHalfBytes, 1024),
+                   idesc_pv, (!first || k > 0) ? 1u : 0u);
+          if (half == 0) mma_commit(bar(B_PVHALF + s));
+        }
+        p_phase ^= 1u << s;
+        return true;
       };
       bool ok = true;
       while (ok && walk.next(p, &w)) {
         if (!wait(bar(B_QREADY), n_piece & 1)) break;
         tc_fence_after();
-        if (NQT == 1) {
-          for (int i = 0; ok && i < 2 && i < w.n; ++i) {
-            if (!(ok = arrived(g))) break;
-            qk(i, g % NST);
-            mma_commit(bar(B_EMPTY + g++ % NST));
-          }
-          for (int i = 0; ok && i < w.n; ++i) {
-            if (!(ok = p_ready(i & 1) && arrived(g))) break;
-            pv(i & 1, g % NST, i < 2);
-            mma_commit(bar(B_EMPTY + g++ % NST));
-            if (i + 2 < w.n) {
-              if (!(ok = arrived(g))) break;
-              qk(i & 1, g % NST);
-              mma_commit(bar(B_EMPTY + g++ % NST));
-            }
-          }
-        } else {
+        for (int i = 0; i < kAhead && i < w.n; ++i) {
           if (!(ok = arrived(g))) break;
-          qk(0, g % NST);
-          qk(1, g % NST);
+          qk(NQT == 1 ? i : 0, g % NST);
+          if (NQT == 2) qk(1, g % NST);
           mma_commit(bar(B_EMPTY + g++ % NST));
-          for (int i = 0; ok && i < w.n; ++i) {
-            const bool more = i + 1 < w.n;
-            const uint32_t gv = g++, gk = more ? g++ : 0;
-            if (!(ok = p_ready(0) && arrived(gv))) break;
-            pv(0, gv % NST, i == 0);
-            if (more) {
-              if (!(ok = arrived(gk))) break;
-              qk(0, gk % NST);
-            }
-            if (!(ok = p_ready(1))) break;
-            pv(1, gv % NST, i == 0);
+        }
+        for (int i = 0; ok && i < w.n; ++i) {
+          const bool more = i + kAhead < w.n;
+          const uint32_t gv = g++, gk = more ? g++ : 0;
+          if (!(ok = pv(NQT == 1 ? i & 1 : 0, gv, i < kAhead))) break;
+          if (NQT == 1) mma_commit(bar(B_EMPTY + gv % NST));
+          if (more) {
+            if (!(ok = arrived(gk))) break;
+            qk(NQT == 1 ? i & 1 : 0, gk % NST);
+            if (NQT == 1) mma_commit(bar(B_EMPTY + gk % NST));
+          }
+          if (NQT == 2) {
+            if (!(ok = pv(1, gv, i == 0))) break;
             mma_commit(bar(B_EMPTY + gv % NST));
             if (more) {
               qk(1, gk % NST);
@@ -239,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     const int cq = lane & 3;
     const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + stream * 128;
     const uint32_t tO = tS + 256;
-    const float c = p.scale_log2, raise = 8.f / c;
+    const float c = p.scale_log2, raise = kRaise / c;
     const uint64_t c2 = pk2(c, c);
     // written by every softmax warp with the same values
     uint64_t* see = reinterpret_cast<uint64_t*>(smem + OFF_SEE);
-    uint32_t g = 0, n_s = 0, n_piece = 0;   // ring tiles and S tiles used so far, pieces
+    uint32_t g = 0, n_t = 0, n_piece = 0;   // ring tiles and this stream's tiles used so far, pieces
     bool ok = true;
     while (ok && walk.next(p, &w)) {
       // ---- the query tiles: eight warps, 16 (32) shared-memory rows each
@@ -284,145 +282,147 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         see[lane + 32] = sv.m1;
         __syncwarp();
       }
-      // running maximum (raw scores) and sum of this thread's rows: A and B of the first half, then of the second
-      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+      // per group of eight rows (A and B of the first half of the lanes, then
+      // of the second): reference score, two partial sums
+      float m[4];
+      uint64_t l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0ull;
+      }
       constexpr int step = NQT == 1 ? 2 : 1;
-      for (int i = NQT == 1 ? stream : 0; i < w.n; i += step) {
-        if (!(ok = wait(bar(B_SFULL + stream), n_s & 1))) break;
-        tc_fence_after();
+      for (int i = NQT == 1 ? stream : 0; i < w.n; i += step, ++n_t) {
         const int k0 = (w.t0 + i) * BN;             // first slot of the tile
-        // one or two halves of 16 lanes; after each, the halves' states change places
-        const int halves = groups > 2 ? 2 : groups > 0 ? 1 : 0;
-#pragma unroll 1
-        for (int hf = 0; hf < halves; ++hf) {
-          const bool both = groups > 2 * hf + 1;
-          const uint32_t tSh = tS + ((uint32_t)(16 * hf) << 16), tOh = tO + ((uint32_t)(16 * hf) << 16);
-          // s[4j + e]: row A, slot k0 + 8j + 2cq + e; s[4j + 2 + e]: row B
-          uint32_t s[64];
-          tmem_ld_16x256b_x8(tSh, *reinterpret_cast<uint32_t(*)[32]>(s));
-          tmem_ld_16x256b_x8(tSh + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-          tmem_wait_ld();
-          if (k0 + BN > w.len) {
-            const int rA = srow0 + 4 * (16 * hf + (lane >> 2)) + quarter;
-            const uint64_t seeA = see[rA % p.T], seeB = see[(rA + 32) % p.T];
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int d = k0 + 8 * j + 2 * cq + e - w.len;      // drafted token of the slot
-                const uint32_t sh = (uint32_t)d & 63u;
-                if (d >= 0 && (d >= 64 || !((seeA >> sh) & 1))) s[4 * j + e] = __float_as_uint(-INFINITY);
-                if (d >= 0 && (d >= 64 || !((seeB >> sh) & 1))) s[4 * j + 2 + e] = __float_as_uint(-INFINITY);
-              }
-          }
-          auto S = [&](int e) { return __uint_as_float(s[e]); };
-          float a0 = fmaxf(S(0), S(1)), a1 = fmaxf(S(4), S(5)), b0 = fmaxf(S(2), S(3)), b1 = fmaxf(S(6), S(7));
-#pragma unroll
-          for (int j = 2; j < 16; j += 2) {
-            a0 = max3(a0, S(4 * j), S(4 * j + 1));
-            a1 = max3(a1, S(4 * j + 4), S(4 * j + 5));
-            b0 = max3(b0, S(4 * j + 2), S(4 * j + 3));
-            b1 = max3(b1, S(4 * j + 6), S(4 * j + 7));
-          }
-          float xA = fmaxf(a0, a1), xB = fmaxf(b0, b1);
-          xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, 1));
-          xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, 1));
-          xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, 2));
-          xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, 2));
-          // the maximum is raised, and O rescaled, only when it grows by more
-          // than 2^8: O / l is exact all the same, and p stays below 2^8
-          const bool rA = xA > m0 + raise, rB = both && xB > m1 + raise;
-          if (__any_sync(0xffffffffu, rA || rB)) {
-            const float fA = rA ? fast_exp2((m0 - xA) * c) : 1.f, fB = rB ? fast_exp2((m1 - xB) * c) : 1.f;
-            if (rA) {
-              m0 = xA;
-              l0 *= fA;
-            }
-            if (rB) {
-              m1 = xB;
-              l1 *= fB;
-            }
-            if (i >= step) {      // S complete implies the stream's last P V complete
-#pragma unroll 1
-              for (int q = 0; q < 4; ++q) {
-                uint32_t o[16];
-                tmem_ld_16x256b_x4(tOh + 32 * q, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  o[4 * j] = __float_as_uint(__uint_as_float(o[4 * j]) * fA);
-                  o[4 * j + 1] = __float_as_uint(__uint_as_float(o[4 * j + 1]) * fA);
-                  o[4 * j + 2] = __float_as_uint(__uint_as_float(o[4 * j + 2]) * fB);
-                  o[4 * j + 3] = __float_as_uint(__uint_as_float(o[4 * j + 3]) * fB);
-                }
-                tmem_st_16x256b_x4(tOh + 32 * q, o);
-              }
-              tmem_wait_st();
-            }
-          }
-          // The difference is taken before the scale: scores near the maximum
-          // keep their distance to it exactly, however large they are. A row
-          // that has seen nothing yet keeps m = -inf: its p are 0.
-          const float nA = m0 == -INFINITY ? 0.f : -m0, nB = m1 == -INFINITY ? 0.f : -m1;
-          const uint64_t nA2 = pk2(nA, nA), nB2 = pk2(nB, nB);
-          uint64_t sA = 0ull, sB = 0ull;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            // pk[2u]: row A, pk[2u + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
-            uint32_t pk[16];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int j = 8 * q + u;
-              float x0, x1;
-              unpk2(mul2(add2(pk2(S(4 * j), S(4 * j + 1)), nA2), c2), x0, x1);
-              x0 = fast_exp2(x0);
-              x1 = fast_exp2(x1);
-              sA = add2(sA, pk2(x0, x1));
-              pk[2 * u] = pack_bf16x2(x0, x1);
-              pk[2 * u + 1] = 0u;
-            }
-            if (both) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const int j = 8 * q + u;
-                float x0, x1;
-                unpk2(mul2(add2(pk2(S(4 * j + 2), S(4 * j + 3)), nB2), c2), x0, x1);
-                x0 = fast_exp2(x0);
-                x1 = fast_exp2(x1);
-                sB = add2(sB, pk2(x0, x1));
-                pk[2 * u + 1] = pack_bf16x2(x0, x1);
-              }
-            }
-            tmem_st_16x128b_x8(tSh + 32 * q, pk);
-          }
-          float x0, x1;
-          unpk2(sA, x0, x1);
-          l0 += x0 + x1;
-          unpk2(sB, x0, x1);
-          l1 += x0 + x1;
-          if (halves == 2) {
-            float y;
-            y = m0; m0 = m2; m2 = y;
-            y = m1; m1 = m3; m3 = y;
-            y = l0; l0 = l2; l2 = y;
-            y = l1; l1 = l3; l3 = y;
-          }
-        }
         // V rows past the last slot: zero them before the product reads them
         const int slots = w.len + w.draft;
         if (k0 + BN > slots && (NQT == 1 || stream == 0)) {
           const uint32_t q = g + 2 * w.n - 1;      // the item's last tile is the piece's last load
           if (!(ok = wait(bar(B_FULL + q % NST), (q / NST) & 1))) break;
-          unsigned char* v = smem + (NQT + q % NST) * kTileBytes;
+          unsigned char* v = smem + NQT * kTileBytes + (q % NST) * kKvBytes;
           for (int x = (slots - k0) * 16 + quarter * 32 + lane; x < BN * 16; x += 128)
-            *reinterpret_cast<uint4*>(v + (x & 1) * kHalfBytes + (x >> 1) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(v + (x & 1) * kKvHalfBytes + (x >> 1) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_PREADY + stream));
-        ++n_s;
+        if (!(ok = wait(bar(B_SFULL + stream), n_t & 1))) break;
+        tc_fence_after();
+        // two halves of 64 slots; P of a half goes over S of the first one
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (groups > 0) {
+            const uint32_t tSh = tS + half * 64, tP = tS + half * 32;
+            // s[32 hf + 4j + e]: row A of lane half hf, slot k0 + 64 half + 8j + 2cq + e; + 2: row B
+            uint32_t s[64];
+            tmem_ld_16x256b_x8(tSh, *reinterpret_cast<uint32_t(*)[32]>(s));
+            if (groups > 2) tmem_ld_16x256b_x8(tSh + (16u << 16), *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            tmem_wait_ld();
+            auto S = [&](int gr, int j, int e) -> uint32_t& { return s[32 * (gr >> 1) + 4 * j + 2 * (gr & 1) + e]; };
+            const int n0 = w.len - k0 - 64 * half;      // slots of the half that hold cached keys
+            if (n0 < 64) {
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                if (groups <= gr) break;
+                const uint64_t sees = see[(srow0 + 4 * (8 * gr + (lane >> 2)) + quarter) % p.T];
+                uint64_t vis = n0 > 0 ? (sees << n0) | ((1ull << n0) - 1) : n0 > -64 ? sees >> -n0 : 0ull;
+                vis >>= 2 * cq;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (!((vis >> (8 * j + e)) & 1)) S(gr, j, e) = __float_as_uint(-INFINITY);
+              }
+            }
+            // Scores are taken relative to a reference of the row, its
+            // largest score when the reference was last set: it is set again,
+            // and O rescaled, only when a score passes it by 2^kRaise. P and
+            // the sums have fp32's exponent range, so O / l is the same; the
+            // test needs no exchange between the row's threads.
+            float x[4];
+            bool up = false;
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr) {
+              x[gr] = -INFINITY;
+              if (groups <= gr) continue;
+              auto F = [&](int j, int e) { return __uint_as_float(S(gr, j, e)); };
+              float a0 = fmaxf(F(0, 0), F(0, 1)), a1 = fmaxf(F(1, 0), F(1, 1));
+#pragma unroll
+              for (int j = 2; j < 8; j += 2) {
+                a0 = max3(a0, F(j, 0), F(j, 1));
+                a1 = max3(a1, F(j + 1, 0), F(j + 1, 1));
+              }
+              x[gr] = fmaxf(a0, a1);
+              up = up || x[gr] > m[gr] + raise;
+            }
+            if (__any_sync(0xffffffffu, up)) {
+              float f[4];
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                x[gr] = fmaxf(x[gr], __shfl_xor_sync(0xffffffffu, x[gr], 1));
+                x[gr] = fmaxf(x[gr], __shfl_xor_sync(0xffffffffu, x[gr], 2));
+                const bool r = x[gr] > m[gr] + raise;
+                f[gr] = r ? fast_exp2((m[gr] - x[gr]) * c) : 1.f;
+                if (r) m[gr] = x[gr];
+                l[gr] = mul2(l[gr], pk2(f[gr], f[gr]));
+              }
+              // S complete implies the products of the stream's earlier tiles complete
+              if (half == 1 && !(ok = wait(bar(B_PVHALF + stream), n_t & 1))) break;
+              tc_fence_after();
+              if (i >= step || half == 1) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                  if (groups <= 2 * hf) break;
+                  const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
+#pragma unroll 1
+                  for (int q = 0; q < 4; ++q) {
+                    uint32_t o[16];
+                    tmem_ld_16x256b_x4(tOh + 32 * q, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                      o[j] = __float_as_uint(__uint_as_float(o[j]) * f[2 * hf + ((j >> 1) & 1)]);
+                    tmem_st_16x256b_x4(tOh + 32 * q, o);
+                  }
+                }
+                tmem_wait_st();
+              }
+            }
+            // The difference is taken before the scale: scores near the
+            // reference keep their distance to it exactly, however large they
+            // are. A row that has seen nothing yet keeps m = -inf: its p are 0.
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              if (groups <= 2 * hf) break;
+              // pk[2j]: row A, pk[2j + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
+              uint32_t pk[16];
+#pragma unroll
+              for (int ab = 0; ab < 2; ++ab) {
+                const int gr = 2 * hf + ab;
+                if (groups > gr) {
+                  const float n = m[gr] == -INFINITY ? 0.f : -m[gr];
+                  const uint64_t n2 = pk2(n, n);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    float x0, x1;
+                    unpk2(mul2(add2(pk2(__uint_as_float(S(gr, j, 0)), __uint_as_float(S(gr, j, 1))), n2), c2), x0, x1);
+                    x0 = fast_exp2(x0);
+                    x1 = fast_exp2(x1);
+                    l[gr] = add2(l[gr], pk2(x0, x1));
+                    pk[2 * j + ab] = pack_bf16x2(x0, x1);
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) pk[2 * j + ab] = 0u;
+                }
+              }
+              tmem_st_16x128b_x8(tP + ((uint32_t)(16 * hf) << 16), pk);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_PREADY + 2 * stream + half));
+        }
+        if (!ok) break;
       }
       if (!ok) break;
       g += 2 * w.n;
@@ -436,15 +436,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       for (int hf = 0; hf < 2; ++hf) {
         if (groups <= 2 * hf) break;
         const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
-        float lA = hf ? l2 : l0, lB = hf ? l3 : l1;
+        float lA, lB, y;
+        unpk2(l[2 * hf], lA, y);
+        lA += y;
+        unpk2(l[2 * hf + 1], lB, y);
+        lB += y;
         lA += __shfl_xor_sync(0xffffffffu, lA, 1);
         lB += __shfl_xor_sync(0xffffffffu, lB, 1);
         lA += __shfl_xor_sync(0xffffffffu, lA, 2);
         lB += __shfl_xor_sync(0xffffffffu, lB, 2);
         const int ra = 4 * (16 * hf + (lane >> 2)) + quarter, rb = ra + 32;     // rows within the tile
         if (cq == 0) {
-          if (ra < srows) p.part_ml[slot * p.row_cap + ra] = make_float2(hf ? m2 : m0, lA);
-          if (rb < srows) p.part_ml[slot * p.row_cap + rb] = make_float2(hf ? m3 : m1, lB);
+          if (ra < srows) p.part_ml[slot * p.row_cap + ra] = make_float2(m[2 * hf], lA);
+          if (rb < srows) p.part_ml[slot * p.row_cap + rb] = make_float2(m[2 * hf + 1], lB);
         }
         if (used) {
           float* oa = p.part_o + (slot * p.row_cap + ra) * kHeadDim + 2 * cq;
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kHeadDim) tree_combine_kernel(const TreeParams
       sum_before += __reduce_add_sync(0xffffffffu, b0 + lane < b ? n : 0);
     }
     const long long per = (long long)p.Hkv * p.blocks, total = per * sum_all;
-    const int nt = (s.len + s.draft + BN - 1) / BN;
+    const int nt = key_tiles(p, s);
     const long long a = per * sum_before + ((long long)h * p.blocks + block) * nt, e = a + nt;
     const int item = bh * p.blocks + block;
     // the CTAs whose shares [total c / grid, total (c + 1) / grid) meet [a, e)
@@ -591,7 +595,7 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   EncodeTiledFn enc = tmap_encode_fn();
   if (!enc) return cuda_status(cudaErrorNotSupported);
   TreeMaps maps;
-  if (!make_cache_map(enc, &maps.k, K, ks, B, Hkv, cap) || !make_cache_map(enc, &maps.v, V, vs, B, Hkv, cap))
+  if (!make_cache_map(enc, &maps.k, K, ks, B, Hkv, cap, BN) || !make_cache_map(enc, &maps.v, V, vs, B, Hkv, cap, BN))
     return DHSA_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -622,6 +626,7 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.blocks = q.blocks;
   p.row_cap = q.row_cap;
   p.every = false;
+  p.tile = BN;
   const long long most = (long long)B * Hkv * q.blocks * ceil_div(cap, BN);   // tiles at full lengths
   p.grid = sms < kMaxGrid ? sms : kMaxGrid;
   if (most < p.grid) p.grid = (int)most;
@@ -634,10 +639,13 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   if (st == DHSA_OK && weight_out) {
     p.every = true;                   // weights without new tokens are passed on
     p.blocks = 1;                     // one walk over the keys for all rows of a head
+    p.tile = tree_weight_tile();
     p.grid = sms < kMaxGrid ? sms : kMaxGrid;
-    const long long tiles = (long long)B * Hkv * ceil_div(cap, BN);
+    const long long tiles = (long long)B * Hkv * ceil_div(cap, p.tile);
     if (tiles < p.grid) p.grid = (int)tiles;
-    st = launch_tree_weight(maps.k, p, stream);
+    CUtensorMap kmap;
+    if (!make_cache_map(enc, &kmap, K, ks, B, Hkv, cap, p.tile)) return DHSA_ERR_INVALID_ARG;
+    st = launch_tree_weight(kmap, p, stream);
   }
   return st;
 }

@@ -18,6 +18,9 @@ namespace dhsa {
 namespace {
 
 constexpr int kThreads = 384;
+constexpr int BN = 128;                      // slots per key tile
+constexpr uint32_t kHalfBytes = BN * 128;    // 128 rows x 64 bf16, 128-byte swizzle
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr int kRowBlock = 256;               // rows per walk: columns of an S^T buffer
 constexpr uint32_t kQHalfBytes = kRowBlock * 128;
 constexpr int kStages = 4;
@@ -261,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
 }
 
 }  // namespace
+
+int tree_weight_tile() { return BN; }
 
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream) {
   const cudaError_t e =
