@@ -9,6 +9,7 @@ loudly (build it with `python -m long_context_prefill_dhsa_b200.build`).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -411,34 +412,74 @@ def sparse_attn_fwd_noalloc(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, o
 
 
 # ----------------------------------------------------------------- rotary positions and the cache
-def _on(t: Optional[torch.Tensor], dtype, shape, name: str, device):
+# These calls are made once per new token, so their checks are kept cheap: one
+# pass that accepts, and the reasons only for what it does not.
+_raw_stream = torch._C._cuda_getCurrentRawStream     # current stream of a device, as an address
+
+
+def _on(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
     """A dense tensor of the call, on the call's device; returns its pointer (None for None)."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device \
+            and t.is_contiguous():
+        return t.data_ptr()
     _need(t, dtype, shape, name)
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
 
 
-def _rows(t: Optional[torch.Tensor], shape, name: str, device):
+def _rows(t: Optional[torch.Tensor], shape, name: str, device: int):
     """A [B, H, rows, 128] bf16 tensor with contiguous rows and any strides:
     returns its pointer and its strides for the library (None when dense)."""
     if t is None:
         return None, None
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), None
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
+        return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: on {t.device}, expected {device if device.type == 'cuda' else 'a CUDA device'}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _call_device(t: torch.Tensor, name: str) -> int:
+    """Device number of the call's first tensor, a CUDA tensor of four dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise TypeError(f"{name}: expected a tensor of four dimensions")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.get_device()
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(B: int, Hq: int, Hkv: int, T: int, cap: int, want_weight: bool) -> int:
+    return load().dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, want_weight)
+
+
+@functools.lru_cache(maxsize=256)
+def _evict_workspace(B: int, Hkv: int, cap: int) -> int:
+    return load().dhsa_cache_evict_workspace_size(B, Hkv, cap)
+
+
+def _workspace(t: Optional[torch.Tensor], size: int, device: int):
+    """Pointer and bytes of the caller's workspace, or of a new one (kept by the returned tensor)."""
+    if t is None:
+        t = torch.empty(size, dtype=torch.uint8, device=device)
+        return t, t.data_ptr(), size
+    _need(t, t.dtype, None, "workspace")
+    if t.get_device() != device:
+        raise ValueError(f"workspace: on {t.device}, expected cuda:{device}")
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
 def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: torch.Tensor,
@@ -460,10 +501,8 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
     ref = next((x for x in (Q, K, V) if x is not None), None)
     if ref is None:
         raise ValueError("rotary_qkv: Q, K and V are all None")
-    if not isinstance(ref, torch.Tensor) or ref.dim() != 4:
-        raise TypeError("rotary_qkv: expected tensors [B, H, T, 128]")
-    device = ref.device
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    device = _call_device(ref, "Q" if Q is not None else "K" if K is not None else "V")
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return rotary_qkv(Q, K, inv_freq, V, positions, start, n_new, slots, interleaved, transpose, factor,
                               Q_out, K_out, V_out, pos_out)
@@ -490,12 +529,12 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
     if positions is not None and start is not None:
         raise ValueError("rotary_qkv: positions and start exclude each other")
     _check(load().dhsa_rotary_qkv(
-        q, qs, k, ks, v, vs, B, Hq, Hkv, T, d, _on(inv_freq, torch.float64, None, "inv_freq", device),
+        q, qs, k, ks, v, vs, B, Hq, Hkv, T, d, _on(inv_freq, torch.float64, (inv_freq.numel(),), "inv_freq", device),
         2 * inv_freq.numel(), bool(interleaved), bool(transpose), factor,
         _on(positions, torch.int32, (B, T), "positions", device), _on(start, torch.int32, (B,), "start", device),
         _on(n_new, torch.int32, (B,), "n_new", device), qo, ko, kos, vo, vos,
         _on(slots, torch.int32, (B,), "slots", device), cap,
-        _on(pos_out, torch.int32, (B, Hkv, cap), "pos_out", device), _stream_ptr()), "dhsa_rotary_qkv")
+        _on(pos_out, torch.int32, (B, Hkv, cap), "pos_out", device), _raw_stream(device)), "dhsa_rotary_qkv")
     return Q_out, K_out, V_out
 
 
@@ -516,16 +555,15 @@ def tree_attn(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lengths: torch.
     (None: a chain; T = 1 is plain decoding). With `weight` (fp32 [B,Hkv,cap])
     each slot's attention weight is added to it, into weight_out (None: in
     place). Returns out (bf16, like Q)."""
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or not isinstance(K, torch.Tensor) or K.dim() != 4:
-        raise TypeError("tree_attn: expected Q [B, Hq, T, 128] and caches [B, Hkv, cap, 128]")
-    device = Q.device
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    device = _call_device(Q, "Q")
+    _call_device(K, "K")
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return tree_attn(Q, K, V, lengths, parents, n_draft, softmax_scale, weight, weight_out, out, lse,
                              workspace)
     B, Hq, T, d = Q.shape
     Hkv, cap = K.shape[1], K.shape[2]
-    q = _on(Q, torch.bfloat16, None, "Q", device)
+    q = _on(Q, torch.bfloat16, (B, Hq, T, d), "Q", device)
     k, ks = _rows(K, (B, Hkv, cap, d), "K", device)
     v, vs = _rows(V, (B, Hkv, cap, d), "V", device)
     if weight is None and weight_out is not None:
@@ -534,19 +572,15 @@ def tree_attn(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lengths: torch.
         weight_out = weight
     if out is None:
         out = torch.empty_like(Q)
-    lib = load()
-    if workspace is None:
-        workspace = torch.empty(lib.dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, weight is not None),
-                                dtype=torch.uint8, device=device)
-    _check(lib.dhsa_tree_attn(
+    workspace, ws, ws_bytes = _workspace(workspace, _tree_workspace(B, Hq, Hkv, T, cap, weight is not None), device)
+    _check(load().dhsa_tree_attn(
         q, k, ks, v, vs, B, Hq, Hkv, T, cap, d, _on(lengths, torch.int32, (B,), "lengths", device),
         _on(parents, torch.int32, (B, T), "parents", device), _on(n_draft, torch.int32, (B,), "n_draft", device),
         1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale),
         _on(out, torch.bfloat16, (B, Hq, T, d), "out", device), _on(lse, torch.float32, (B, Hq, T), "lse", device),
         _on(weight, torch.float32, (B, Hkv, cap), "weight", device),
-        _on(weight_out, torch.float32, (B, Hkv, cap), "weight_out", device),
-        _on(workspace, workspace.dtype, None, "workspace", device), workspace.numel() * workspace.element_size(),
-        _stream_ptr()), "dhsa_tree_attn")
+        _on(weight_out, torch.float32, (B, Hkv, cap), "weight_out", device), ws, ws_bytes, _raw_stream(device)),
+        "dhsa_tree_attn")
     return out
 
 
@@ -565,10 +599,8 @@ def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: tor
     Slots with pos < sinks or pos >= next_pos - recent rank first. index
     (int32 [B,Hkv,min(keep,cap)]) receives each slot's source.
     Returns lengths_out (a new tensor unless given; not `lengths` itself)."""
-    if not isinstance(K, torch.Tensor) or K.dim() != 4:
-        raise TypeError("cache_evict: expected caches [B, Hkv, cap, 128]")
-    device = K.device
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    device = _call_device(K, "K")
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return cache_evict(K, V, weight, pos, lengths, keep, next_pos, n_draft, accept, sinks, recent, weight_out,
                                pos_out, lengths_out, index, workspace)
@@ -582,10 +614,8 @@ def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: tor
     if lengths_out is None:
         lengths_out = torch.empty_like(lengths)
     keep = min(int(keep), 0x7fffffff)
-    lib = load()
-    if workspace is None:
-        workspace = torch.empty(lib.dhsa_cache_evict_workspace_size(B, Hkv, cap), dtype=torch.uint8, device=device)
-    _check(lib.dhsa_cache_evict(
+    workspace, ws, ws_bytes = _workspace(workspace, _evict_workspace(B, Hkv, cap), device)
+    _check(load().dhsa_cache_evict(
         k, ks, v, vs, _on(weight, torch.float32, (B, Hkv, cap), "weight", device),
         _on(pos, torch.int32, (B, Hkv, cap), "pos", device), B, Hkv, cap, d,
         _on(lengths, torch.int32, (B,), "lengths", device), _on(n_draft, torch.int32, (B,), "n_draft", device),
@@ -594,9 +624,8 @@ def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: tor
         _on(weight_out, torch.float32, (B, Hkv, cap), "weight_out", device),
         _on(pos_out, torch.int32, (B, Hkv, cap), "pos_out", device),
         _on(lengths_out, torch.int32, (B,), "lengths_out", device),
-        _on(index, torch.int32, (B, Hkv, min(keep, cap)), "index", device),
-        _on(workspace, workspace.dtype, None, "workspace", device), workspace.numel() * workspace.element_size(),
-        _stream_ptr()), "dhsa_cache_evict")
+        _on(index, torch.int32, (B, Hkv, min(keep, cap)), "index", device), ws, ws_bytes, _raw_stream(device)),
+        "dhsa_cache_evict")
     return lengths_out
 
 

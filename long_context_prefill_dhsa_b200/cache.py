@@ -87,9 +87,11 @@ class KVCache:
         self.lengths = torch.zeros(B, dtype=torch.int32, device=dev)
         self._lengths_next = torch.zeros_like(self.lengths)
         self.next_pos = torch.zeros_like(self.lengths)
+        # what a step needs depends on its number of tokens, and not only upwards
         self._ws = torch.empty(max(
-            lib.dhsa_tree_attn_workspace_size(B, Hq, Hkv, lib.dhsa_tree_max_drafts(), cap, track_weight),
-            lib.dhsa_cache_evict_workspace_size(B, Hkv, cap)), dtype=torch.uint8, device=dev)
+            lib.dhsa_cache_evict_workspace_size(B, Hkv, cap),
+            *(lib.dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, track_weight)
+              for T in range(1, lib.dhsa_tree_max_drafts() + 1))), dtype=torch.uint8, device=dev)
         self._bits = torch.arange(lib.dhsa_tree_max_drafts(), dtype=torch.int64, device=dev)
         self._prompt: Optional[int] = None      # tokens of a prompt that nothing has followed yet
         self._arange = torch.arange(cap, dtype=torch.int32, device=dev)

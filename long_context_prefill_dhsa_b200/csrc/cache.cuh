@@ -44,6 +44,33 @@ inline bool make_cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The current device's number and SM count, looked up once per device.
+inline cudaError_t this_device(int* dev, int* sms) {
+  constexpr int kMost = 64;
+  static int count[kMost] = {0};
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  if (*dev < 0 || *dev >= kMost) return cudaErrorInvalidDevice;
+  if (count[*dev] == 0) {
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) return e;
+    count[*dev] = n;
+  }
+  *sms = count[*dev];
+  return cudaSuccess;
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device and kernel
+// (`done`: a static array of 64 flags beside the launch).
+template <typename F>
+inline cudaError_t allow_smem(F* kernel, int bytes, int dev, bool* done) {
+  if (done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
 // A sequence's cached slots and drafted tokens, clamped into the cache.
 struct SeqLen {
   int len, draft;

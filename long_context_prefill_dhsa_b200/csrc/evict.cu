@@ -5,8 +5,8 @@
 // weight descending, slot ascending). The rank is a 32-bit key whose unsigned
 // order is that of the weights; held slots take the largest key, slots that
 // are no candidates the key 0. The m-th largest key is found by a radix
-// search (digits of 11, 11 and 10 bits from the top, one histogram each);
-// among equal keys the first slots win.
+// search (four 8-bit digits from the top, one histogram each); among equal
+// keys the first slots win.
 //
 // The kept rows must end in slots 0 .. m-1, and the order of slots carries no
 // meaning, so only as many rows move as there are unkept slots below m: the
@@ -17,8 +17,8 @@
 // hold the keys in shared memory, and read each other's histograms and
 // counts through distributed shared memory, so the whole update is one
 // launch. Bound: 8 bytes (weight, position) per slot and 1 KB per moved row
-// against HBM; for small caches the chain of three histogram rounds, two
-// count rounds and their cluster barriers.
+// against HBM; for small caches the chain of four histogram rounds, one round
+// of counts and their barriers.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
@@ -28,11 +28,13 @@ namespace cg = cooperative_groups;
 namespace dhsa {
 namespace {
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kRounds = 3;
-constexpr int kMaxCluster = 8;            // portable cluster size
+constexpr int kBins = 256;
+constexpr int kParts = kEvThreads / kBins;
+constexpr int kRounds = 4;
+constexpr int kMaxCluster = 16;           // above 8 the launch asks for the non-portable size
+constexpr int kBatch = 8;                 // slots whose weight and position a thread loads at a time
 constexpr int kKeysPerBlock = 48 * 1024;  // keys held in shared memory; later ones are derived again
 constexpr int kSlotsPerBlock = 8192;      // slots a block of a cluster is given before another one joins
 
@@ -57,15 +59,40 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct EvictShared {
-  uint32_t hist[kRounds][kBins];
-  uint32_t warp_sum[kEvWarps];
-  uint32_t warp_a[kEvWarps], warp_b[kEvWarps];
-  uint32_t pick_bin, pick_above;
-  uint32_t total[3];         // this block's ties, holes, sources (read by the cluster)
+// counts of one range of slots: keys above the cut and equal to it, in slots
+// below m and from m on
+struct Counts {
+  uint32_t gt_low, eq_low, gt_high, eq_high;
 };
 
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) {
+struct EvictShared {
+  uint32_t hist[kRounds][kBins];
+  uint32_t part[kParts][kBins];
+  uint32_t warp_sum[kBins / 32];
+  uint32_t pick_bin, pick_above, pick_all;
+  Counts warp_count[kEvWarps];
+  Counts total;              // this block's, read by the cluster
+};
+
+// what a range keeps, given how many equal keys before it stay
+struct Kept {
+  uint32_t low, high;
+};
+__device__ __forceinline__ Kept kept_of(const Counts& c, uint32_t eq_before, uint32_t ties) {
+  const uint32_t left = ties > eq_before ? ties - eq_before : 0u;
+  const uint32_t el = min(left, c.eq_low), eh = min(left - el, c.eq_high);
+  return Kept{c.gt_low + el, c.gt_high + eh};
+}
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {     // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams p) {
   extern __shared__ __align__(16) unsigned char ev_smem[];
   EvictShared& sh = *reinterpret_cast<EvictShared*>(ev_smem);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + sizeof(EvictShared));
@@ -95,105 +122,128 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
 
   auto is_cand = [&](int s) { return s < sl.len || ((bits >> (s - sl.len)) & 1ull); };
   auto make_key = [&](int s) -> uint32_t {
-    if (!is_cand(s)) return 0u;
     const int q = pos_in[s];
-    return (q < p.sinks || q >= held_from) ? 0xFFFFFFFFu : weight_key(w_in[s]);
+    const float w = w_in[s];
+    return !is_cand(s) ? 0u : (q < p.sinks || q >= held_from) ? 0xFFFFFFFFu : weight_key(w);
   };
 
   const bool all = m == n_cand;            // every candidate stays: no ranking
   uint32_t cut = 0;                        // the m-th largest key
   uint32_t ties = 0;                       // how many of the slots with that key stay
+  auto key_of = [&](int s) { return s - blk0 < p.keys_held ? keys[s - blk0] : make_key(s); };
   if (!all) {
     for (int i = tid; i < kRounds * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
-    for (int s = w0 + lane; s < w1; s += 32) {
-      const uint32_t k = make_key(s);
-      if (s - blk0 < p.keys_held) keys[s - blk0] = k;
-      atomicAdd(&sh.hist[0][k >> 21], 1u);
+    for (int s0 = w0; s0 < w1; s0 += 32 * kBatch) {
+      uint32_t k[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int s = s0 + 32 * u + lane;
+        k[u] = s < w1 ? make_key(s) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int s = s0 + 32 * u + lane;
+        if (s0 + 32 * u >= w1) break;
+        if (s < w1 && s - blk0 < p.keys_held) keys[s - blk0] = k[u];
+        if (s < w1) atomicAdd(&sh.hist[0][k[u] >> 24], 1u);
+      }
     }
-  }
-  auto key_of = [&](int s) { return s - blk0 < p.keys_held ? keys[s - blk0] : make_key(s); };
-
-  if (!all) {
     uint32_t left = (uint32_t)m;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
-      const int shift = r == 0 ? 21 : r == 1 ? 10 : 0;
+      const int shift = 24 - 8 * r;
       if (r > 0) {
-        const int above = r == 1 ? 21 : 10;
-        const uint32_t mask = r == 1 ? 0x7FFu : 0x3FFu;
-        for (int s = w0 + lane; s < w1; s += 32) {
+#pragma unroll 4
+        for (int s = w0 + lane; s < w1; s += 32) {       // the lane's own keys
           const uint32_t k = key_of(s);
-          if ((k >> above) == (cut >> above)) atomicAdd(&sh.hist[r][(k >> shift) & mask], 1u);
+          if ((k ^ cut) >> (shift + 8) == 0) atomicAdd(&sh.hist[r][(k >> shift) & 255u], 1u);
         }
       }
       cluster.sync();
-      // suffix sums from the top bin: thread t holds bins 2047-2t and 2046-2t
-      uint32_t c0 = 0, c1 = 0;
-      const int hi = kBins - 1 - 2 * tid;
-      for (int c = 0; c < C; ++c) {
-        const uint32_t* rh = cluster.map_shared_rank(&sh.hist[r][0], c);
-        c0 += rh[hi];
-        c1 += rh[hi - 1];
+      // the cluster's histogram: kParts threads per bin add up every kParts-th block's
+      {
+        uint32_t v = 0;
+        const int bin = tid & 255;
+        for (int c = tid >> 8; c < C; c += kParts) v += cluster.map_shared_rank(&sh.hist[r][0], c)[bin];
+        sh.part[tid >> 8][bin] = v;
       }
-      uint32_t inc = c0 + c1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) sh.warp_sum[warp] = inc;
       __syncthreads();
-      uint32_t before = inc - (c0 + c1);
-      for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
-      // exactly one bin holds the left-th key from the top
-      if (before < left && left <= before + c0) {
-        sh.pick_bin = hi;
-        sh.pick_above = before;
-      } else if (before + c0 < left && left <= before + c0 + c1) {
-        sh.pick_bin = hi - 1;
-        sh.pick_above = before + c0;
+      uint32_t n = 0, inc = 0;
+      const int bin = kBins - 1 - tid;          // from the top
+      if (tid < kBins) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) n += sh.part[i][bin];
+        inc = warp_scan(n, lane);
+        if (lane == 31) sh.warp_sum[warp] = inc;
+      }
+      __syncthreads();
+      if (tid < kBins) {
+        uint32_t before = inc - n;
+#pragma unroll
+        for (int i = 0; i < kBins / 32; ++i) before += i < warp ? sh.warp_sum[i] : 0u;
+        if (before < left && left <= before + n) {       // exactly one bin
+          sh.pick_bin = bin;
+          sh.pick_above = before;
+          sh.pick_all = left == before + n;
+        }
       }
       __syncthreads();
       cut |= sh.pick_bin << shift;
       left -= sh.pick_above;
-      __syncthreads();
+      if (sh.pick_all && cut != 0) {      // the whole bin stays: the cut lies right below it
+        cut -= 1;
+        left = 0;
+        break;
+      }
     }
     ties = left;
   }
 
-  // an exclusive sum over the cluster's blocks and this block's warps
-  auto warp_offsets = [&](uint32_t* sums, int which) {
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t t = 0;
-      for (int i = 0; i < kEvWarps; ++i) t += sums[i];
-      sh.total[which] = t;
-    }
-  };
-  auto below = [&](const uint32_t* sums, int which) {
-    uint32_t t = 0;
-    for (int c = 0; c < rank; ++c) t += *cluster.map_shared_rank(&sh.total[which], c);
-    for (int i = 0; i < warp; ++i) t += sums[i];
-    return t;
-  };
-
-  uint32_t tie_at = 0;
-  if (!all) {
-    uint32_t n = 0;
-    for (int s0 = w0; s0 < w1; s0 += 32) {
-      const int s = s0 + lane;
-      n += __popc(__ballot_sync(0xffffffffu, s < w1 && key_of(s) == cut));
-    }
-    if (lane == 0) sh.warp_sum[warp] = n;
-    warp_offsets(sh.warp_sum, 0);
-    cluster.sync();
-    tie_at = below(sh.warp_sum, 0);
+  // counts of the warp's slots, then of every range before them
+  Counts mine{0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = w0 + lane; s < w1; s += 32) {
+    const uint32_t k = all ? (is_cand(s) ? 1u : 0u) : key_of(s);
+    const bool low = s < m, gt = k > cut, eq = !all && k == cut;
+    mine.gt_low += gt && low;
+    mine.gt_high += gt && !low;
+    mine.eq_low += eq && low;
+    mine.eq_high += eq && !low;
   }
+  mine.gt_low = __reduce_add_sync(0xffffffffu, mine.gt_low);
+  mine.gt_high = __reduce_add_sync(0xffffffffu, mine.gt_high);
+  mine.eq_low = __reduce_add_sync(0xffffffffu, mine.eq_low);
+  mine.eq_high = __reduce_add_sync(0xffffffffu, mine.eq_high);
+  if (lane == 0) sh.warp_count[warp] = mine;
+  __syncthreads();
+  Counts wc{0, 0, 0, 0};                        // lane l: warp l's
+  if (lane < kEvWarps) wc = sh.warp_count[lane];
+  if (warp == 0) {
+    Counts t;
+    t.gt_low = __reduce_add_sync(0xffffffffu, wc.gt_low);
+    t.gt_high = __reduce_add_sync(0xffffffffu, wc.gt_high);
+    t.eq_low = __reduce_add_sync(0xffffffffu, wc.eq_low);
+    t.eq_high = __reduce_add_sync(0xffffffffu, wc.eq_high);
+    if (lane == 0) sh.total = t;
+  }
+  cluster.sync();
+  Counts bc{0, 0, 0, 0};                        // lane c: block c's
+  if (lane < C) bc = *cluster.map_shared_rank(&sh.total, lane);
+  auto first = [&](uint32_t v, int n) { return __reduce_add_sync(0xffffffffu, lane < n ? v : 0u); };
+  const uint32_t b_eq = bc.eq_low + bc.eq_high, w_eq = wc.eq_low + wc.eq_high;
+  const Kept bk = kept_of(bc, warp_scan(b_eq, lane) - b_eq, ties);
+  const uint32_t eq_block = first(b_eq, rank);
+  const Kept wk = kept_of(wc, eq_block + warp_scan(w_eq, lane) - w_eq, ties);
+  const uint32_t moves = first(bk.high, 32);    // kept slots from m on
+  uint32_t tie_run = eq_block + first(w_eq, warp);
+  uint32_t hole_at = (uint32_t)min(w0, m) - (first(bk.low, rank) + first(wk.low, warp));
+  uint32_t src_at = first(bk.high, rank) + first(wk.high, warp);
+
   const uint32_t lt = (1u << lane) - 1;
   // whether slot s stays; called for 32 consecutive slots by a whole warp, in
   // order, with the running count of equal keys before them
-  auto stays = [&](int s, uint32_t& tie_run) {
+  auto stays = [&](int s) {
     if (all) return s < w1 && is_cand(s);
     const uint32_t k = s < w1 ? key_of(s) : 0u;
     const uint32_t eq = __ballot_sync(0xffffffffu, s < w1 && k == cut);
@@ -202,42 +252,47 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
     return yes;
   };
 
-  uint32_t tie_run = tie_at, holes = 0, srcs = 0;
-  for (int s0 = w0; s0 < w1; s0 += 32) {
-    const int s = s0 + lane;
-    const bool yes = stays(s, tie_run);
-    holes += __popc(__ballot_sync(0xffffffffu, s < m && s < w1 && !yes));
-    srcs += __popc(__ballot_sync(0xffffffffu, s >= m && yes));
-  }
-  if (lane == 0) {
-    sh.warp_a[warp] = holes;
-    sh.warp_b[warp] = srcs;
-  }
-  warp_offsets(sh.warp_a, 1);
-  warp_offsets(sh.warp_b, 2);
-  cluster.sync();
-  uint32_t hole_at = below(sh.warp_a, 1), src_at = below(sh.warp_b, 2);
-
   // the lists, and what stays where it is
   int32_t* hole_list = p.lists + row;
   int32_t* src_list = hole_list + p.cap / 2;   // min(m, n_all - m) <= cap / 2 rows move
   int32_t* idx_row = p.index ? p.index + (long long)bh * p.index_cols : nullptr;
   float* w_out = p.weight_out + row;
   int32_t* pos_out = p.pos_out + row;
-  tie_run = tie_at;
-  for (int s0 = w0; s0 < w1; s0 += 32) {
-    const int s = s0 + lane;
-    const bool yes = stays(s, tie_run);
-    const bool hole = s < m && s < w1 && !yes, src = s >= m && yes;
-    const uint32_t hb = __ballot_sync(0xffffffffu, hole), sb = __ballot_sync(0xffffffffu, src);
-    if (hole) hole_list[hole_at + __popc(hb & lt)] = s;
-    if (src) src_list[src_at + __popc(sb & lt)] = s;
-    hole_at += __popc(hb);
-    src_at += __popc(sb);
-    if (yes && s < m) {
-      if (idx_row) idx_row[s] = s;
-      if (w_out != w_in) w_out[s] = w_in[s];
-      if (pos_out != pos_in) pos_out[s] = pos_in[s];
+  const bool copy_w = w_out != w_in, copy_pos = pos_out != pos_in;
+  for (int s0 = w0; s0 < w1; s0 += 32 * kBatch) {
+    uint32_t here = 0;                 // bit u: slot s0 + 32 u + lane stays where it is
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int s = s0 + 32 * u + lane;
+      if (s0 + 32 * u >= w1) break;
+      const bool yes = stays(s);
+      const bool hole = s < m && s < w1 && !yes, src = s >= m && yes;
+      const uint32_t hb = __ballot_sync(0xffffffffu, hole), sb = __ballot_sync(0xffffffffu, src);
+      if (hole) hole_list[hole_at + __popc(hb & lt)] = s;
+      if (src) src_list[src_at + __popc(sb & lt)] = s;
+      hole_at += __popc(hb);
+      src_at += __popc(sb);
+      if (yes && s < m) here |= 1u << u;
+    }
+    if (s0 >= m || !(copy_w || copy_pos || idx_row)) continue;
+    float wv[kBatch];
+    int32_t pv[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int s = s0 + 32 * u + lane;
+      if ((here >> u) & 1) {
+        wv[u] = w_in[s];
+        pv[u] = pos_in[s];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int s = s0 + 32 * u + lane;
+      if ((here >> u) & 1) {
+        if (idx_row) idx_row[s] = s;
+        if (copy_w) w_out[s] = wv[u];
+        if (copy_pos) pos_out[s] = pv[u];
+      }
     }
   }
   if (idx_row)
@@ -245,46 +300,42 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
   // the cluster's lists are complete, and nobody reads a weight or position
   // to rank it any more
   cluster.sync();
-  uint32_t moves = 0;
-  for (int c = 0; c < C; ++c) moves += *cluster.map_shared_rank(&sh.total[1], c);
   // one warp per moved slot: 16 lanes carry its K row, 16 its V row
   const bool is_v = lane >= 16;
   __nv_bfloat16* base = is_v ? p.V + b * p.vs.b + h * p.vs.h : p.K + b * p.ks.b + h * p.ks.h;
   const long long rs = is_v ? p.vs.r : p.ks.r;
   base += (lane & 15) * 8;
   constexpr int kInFlight = 4;
-  const int stride = C * kEvWarps;
-  for (uint32_t r0 = rank * kEvWarps + warp; r0 < moves; r0 += kInFlight * stride) {
-    uint4 x[kInFlight];
-    int dst[kInFlight], from[kInFlight];
-#pragma unroll
-    for (int k = 0; k < kInFlight; ++k) {
-      const uint32_t r = r0 + k * stride;
-      dst[k] = -1;
-      if (r < moves) {
-        dst[k] = hole_list[r];
-        from[k] = src_list[r];
-        x[k] = *reinterpret_cast<const uint4*>(base + from[k] * rs);
-      }
+  const uint32_t stride = C * kEvWarps;
+  // lane l of a warp holds the l-th of its next 32 moves
+  for (uint32_t r0 = rank * kEvWarps + warp; r0 < moves; r0 += 32 * stride) {
+    const uint32_t at = r0 + lane * stride;
+    const int my_dst = at < moves ? hole_list[at] : -1, my_from = at < moves ? src_list[at] : 0;
+    if (my_dst >= 0) {
+      w_out[my_dst] = w_in[my_from];
+      pos_out[my_dst] = pos_in[my_from];
+      if (idx_row) idx_row[my_dst] = my_from;
     }
+    const int n = __popc(__ballot_sync(0xffffffffu, my_dst >= 0));
+    for (int k0 = 0; k0 < n; k0 += kInFlight) {
+      uint4 x[kInFlight];
 #pragma unroll
-    for (int k = 0; k < kInFlight; ++k) {
-      if (dst[k] < 0) continue;
-      *reinterpret_cast<uint4*>(base + dst[k] * rs) = x[k];
-      if (lane == 0) {
-        w_out[dst[k]] = w_in[from[k]];
-        if (idx_row) idx_row[dst[k]] = from[k];
+      for (int k = 0; k < kInFlight; ++k) {
+        const int from = __shfl_sync(0xffffffffu, my_from, (k0 + k) & 31);
+        if (k0 + k < n) x[k] = *reinterpret_cast<const uint4*>(base + from * rs);
       }
-      if (lane == 16) pos_out[dst[k]] = pos_in[from[k]];
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        const int dst = __shfl_sync(0xffffffffu, my_dst, (k0 + k) & 31);
+        if (k0 + k < n) *reinterpret_cast<uint4*>(base + dst * rs) = x[k];
+      }
     }
   }
-  // no block leaves while another may still read its counts
-  cluster.sync();
 }
 
-int cluster_size(int cap) {
+int cluster_size(int cap, int heads) {
   int c = 1;
-  while (c < kMaxCluster && (long long)c * kSlotsPerBlock < cap) c *= 2;
+  while (c < kMaxCluster && (long long)c * kSlotsPerBlock < cap && (c < 8 || heads * c <= 148)) c *= 2;
   return c;
 }
 
@@ -323,12 +374,16 @@ int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, c
   p.index_cols = keep < cap ? keep : cap;
   p.max_draft = evict_max_drafts();
   p.status = status;
-  const int C = cluster_size(cap);
-  const int span = ceil_div(ceil_div(cap, C * kEvWarps), 32) * 32 * kEvWarps;   // slots of one block at most
+  const int C = cluster_size(cap, B * Hkv);
+  const int span = ceil_div(cap, C * kEvThreads) * kEvThreads;   // slots of one block at most
   p.keys_held = span < kKeysPerBlock ? span : kKeysPerBlock;
   const size_t smem = sizeof(EvictShared) + 4u * (size_t)p.keys_held;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(EvictShared) + 4u * (size_t)kKeysPerBlock));
+  static bool done[64] = {false};
+  int dev = 0, sms = 0;
+  cudaError_t e = this_device(&dev, &sms);
+  if (e == cudaSuccess && !done[dev])
+    e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = allow_smem(evict_kernel, (int)(sizeof(EvictShared) + 4u * (size_t)kKeysPerBlock), dev, done);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * Hkv * C));

@@ -13,16 +13,20 @@ struct TreeParams {
   __nv_bfloat16* O;
   float* lse;
   float2* row_stat;         // per row: largest raw score and 1 / denominator, for the weight pass (null without)
-  float* part_o;            // [piece][stream][row_cap][128]
-  float2* part_ml;          // [piece][stream][row_cap]: running maximum of the raw scores, and sum
+  float* scores;            // [B * Hkv][rows][score_cap] raw scores for the weight pass, or null
+  float* part_o;            // [piece][query tile][row_cap][128]
+  float2* part_ml;          // [piece][query tile][row_cap]: reference score and sum
   const float* weight;
   float* weight_out;
   int B, Hq, Hkv, G, T, cap;
   int rows;                 // G * T
   int blocks;               // query blocks of a kv head that walk the keys
-  int row_cap;              // rows of a stream's partial
+  int row_cap;              // rows of a query tile's partial
+  int score_cap;            // cap rounded up to whole key tiles
   int tile;                 // slots of a key tile
   int grid;                 // CTAs that share the key tiles
+  bool whole;               // items are not split: the line counts items instead of key tiles
+  bool keep_k;              // K is read again after this kernel
   bool every;               // sequences without drafted tokens are walked too
   float scale, scale_log2;
   unsigned int* status;
@@ -34,16 +38,21 @@ using namespace ptx;
 
 constexpr int kMaxDrafts = 64;   // one bit of a 64-bit word each
 constexpr int kMaxGroup = 64;    // query heads of one kv head
+constexpr int kMaxScoreRows = 32;   // rows of a head up to which the attention keeps its scores for the weight pass
 constexpr int kMaxGrid = 160;    // CTAs (one per SM) the workspace is sized for
 
 constexpr uint32_t kTmemCols = 512;
 
-// key tiles of each item of sequence b
+// key tiles of each item of a sequence, and the item's length on the line
 __device__ __forceinline__ int key_tiles(const TreeParams& p, const SeqLen& s) {
   return s.draft > 0 || p.every ? (s.len + s.draft + p.tile - 1) / p.tile : 0;
 }
-__device__ __forceinline__ int key_tiles(const TreeParams& p, int b) {
-  return key_tiles(p, seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap));
+__device__ __forceinline__ int line_len(const TreeParams& p, const SeqLen& s) {
+  const int n = key_tiles(p, s);
+  return p.whole ? min(n, 1) : n;
+}
+__device__ __forceinline__ int line_len(const TreeParams& p, int b) {
+  return line_len(p, seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap));
 }
 
 // The line of key tiles: sequence b's items start at `base`.
@@ -58,7 +67,7 @@ __device__ __forceinline__ Line find_share(const TreeParams& p, int c, int lane)
   Line L;
   const long long per = (long long)p.Hkv * p.blocks;
   int sum = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) sum += b0 + lane < p.B ? key_tiles(p, b0 + lane) : 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) sum += b0 + lane < p.B ? line_len(p, b0 + lane) : 0;
   L.total = per * __reduce_add_sync(0xffffffffu, sum);
   L.start = L.total * c / p.grid;
   L.end = L.total * (c + 1) / p.grid;
@@ -66,7 +75,7 @@ __device__ __forceinline__ Line find_share(const TreeParams& p, int c, int lane)
   L.b = 0;
   long long run = 0;
   for (int b0 = 0; b0 < p.B && run <= L.start; b0 += 32) {
-    const int n = b0 + lane < p.B ? key_tiles(p, b0 + lane) : 0;
+    const int n = b0 + lane < p.B ? line_len(p, b0 + lane) : 0;
     int inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -88,6 +97,7 @@ __device__ __forceinline__ Line find_share(const TreeParams& p, int c, int lane)
 struct Piece {
   int b, h, block;
   int t0, n;            // key tiles t0 .. t0 + n - 1 of the item
+  bool complete;        // they are all of its tiles
   int len, draft;
   int item;
 };
@@ -103,7 +113,7 @@ struct Pieces {
     int nt;
     for (;; ++b) {      // pos < end: a sequence with tiles follows
       s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-      nt = key_tiles(p, s);
+      nt = line_len(p, s);
       if (pos < base + nt * per) break;
       base += nt * per;
     }
@@ -114,11 +124,13 @@ struct Pieces {
     o->block = in_b % p.blocks;
     o->t0 = rel % (unsigned)nt;
     const long long left = end - pos;
-    o->n = (int)min((long long)(nt - o->t0), left);
+    const int n = (int)min((long long)(nt - o->t0), left);
+    o->complete = n == nt;
+    o->n = p.whole ? key_tiles(p, s) : n;
     o->len = s.len;
     o->draft = s.draft;
     o->item = (b * p.Hkv + o->h) * p.blocks + o->block;
-    pos += o->n;
+    pos += n;
     return true;
   }
 };
@@ -224,6 +236,23 @@ struct Waits {
     return false;
   }
 };
+
+// Launches a kernel that may start while the one before it on the stream
+// ends; the kernel itself waits (wait_for_predecessors) before it reads results.
+template <typename... P, typename... A>
+inline int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
 
 }  // namespace
 }  // namespace dhsa

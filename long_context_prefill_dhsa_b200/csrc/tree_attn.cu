@@ -15,8 +15,9 @@
 //   are one line, cut into equal shares, one per CTA of a persistent grid; a
 //   share covers the end of one item, some whole ones and the start of
 //   another. Lengths are read on the device, so ragged batches balance
-//   without host help. Each piece of an item leaves an unnormalised O with
-//   its running maximum and sum, and a second kernel joins an item's pieces.
+//   without host help. A CTA that has all of an item writes its rows; the
+//   others leave an unnormalised O with its reference score and sum for each
+//   piece, and a second kernel joins an item's pieces.
 // * Two softmax streams per CTA, each with its own S and O in TMEM (4 x 128
 //   columns) and its own four warps. With up to 128 rows they take the even
 //   and the odd key tiles of the same query tile; with more they take two
@@ -41,6 +42,7 @@
 namespace dhsa {
 
 int tree_weight_tile();
+int launch_tree_weight_scores(const TreeParams& p, cudaStream_t stream);
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream);
 
 namespace {
@@ -52,6 +54,9 @@ constexpr uint32_t kHalfBytes = BM * 128;    // 128 query rows x 64 bf16, 128-by
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr uint32_t kKvHalfBytes = BN * 128;
 constexpr uint32_t kKvBytes = 2 * kKvHalfBytes;
+// Caches of up to this many key tiles are not split: a CTA takes whole items
+// and writes O itself, which saves the joining kernel.
+constexpr int kWholeTiles = 8;
 constexpr float kRaise = 20.f;   // powers of two by which a score may pass its row's reference
 constexpr uint32_t kSmemData = 224 * 1024;   // query tiles (one or two of 32 KB), the rest is the ring of K and V tiles
 constexpr int kMaxStages = (kSmemData - kTileBytes) / kKvBytes;
@@ -69,13 +74,15 @@ enum {
   B_PREADY = B_SFULL + 2,       // [stream][half]: P of 64 slots written
   B_PVHALF = B_PREADY + 4,      // per stream: P V of a tile's first half complete
   B_OFINAL = B_PVHALF + 2,      // every MMA of the piece complete
-  B_FINAL,
+  B_XCHG,                       // per lane quarter: stream 1's references and sums written
+  B_FINAL = B_XCHG + 4,
   B_TEARDOWN,
   B_COUNT
 };
 constexpr uint32_t OFF_BAR = kSmemData;
 constexpr uint32_t OFF_SEE = OFF_BAR + 8 * ((B_COUNT + 1) & ~1);   // drafted tokens that each drafted token sees
-constexpr uint32_t OFF_LINE = OFF_SEE + kMaxDrafts * 8;
+constexpr uint32_t OFF_XCHG = OFF_SEE + kMaxDrafts * 8;            // per row of the tile: stream 1's reference and sum
+constexpr uint32_t OFF_LINE = OFF_XCHG + BM * 8;
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;   // slack for aligning the base
@@ -113,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         mbar_init(bar(B_PVHALF + s), 1);
       }
       mbar_init(bar(B_OFINAL), 1);
+      for (int s = 0; s < 4; ++s) mbar_init(bar(B_XCHG + s), 1);
       mbar_init(bar(B_FINAL), 1);
       mbar_init(bar(B_TEARDOWN), kThreads / 32 - 1);
       fence_mbar_init();
@@ -133,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR);
   const Waits wait{abort_flag, p.status};
   Pieces walk{line->start, line->end, line->base, line->b};
@@ -140,6 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 
   if (warp == W_PRODUCER) {
     if (lane == 0) {
+      // keys and values are read once (per query block) and must not push
+      // everything else out of L2; K stays where the weight pass reads it again
+      const uint64_t v_policy = p.blocks > 1 ? l2_evict_normal() : l2_evict_first();
+      const uint64_t k_policy = p.keep_k || p.blocks > 1 ? l2_evict_normal() : l2_evict_first();
       uint32_t g = 0;     // tiles loaded
       bool ok = true;
       auto load = [&](const CUtensorMap* m, int tile) {
@@ -147,8 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (g >= NST && !wait(bar(B_EMPTY + st), (g / NST - 1) & 1)) return false;
         const uint32_t dst = ring + st * kKvBytes;
         mbar_arrive_expect_tx(bar(B_FULL + st), kKvBytes);
-        tma_load_4d(dst, m, bar(B_FULL + st), 0, tile * BN, w.h, w.b);
-        tma_load_4d(dst + kKvHalfBytes, m, bar(B_FULL + st), 64, tile * BN, w.h, w.b);
+        const uint64_t policy = m == &maps.k ? k_policy : v_policy;
+        tma_load_4d(dst, m, bar(B_FULL + st), 0, tile * BN, w.h, w.b, policy);
+        tma_load_4d(dst + kKvHalfBytes, m, bar(B_FULL + st), 64, tile * BN, w.h, w.b, policy);
         ++g;
         return true;
       };
@@ -332,6 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                     if (!((vis >> (8 * j + e)) & 1)) S(gr, j, e) = __float_as_uint(-INFINITY);
               }
             }
+            if (NQT == 1 && p.scores) {      // for the weight pass
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                const int r = 4 * (8 * gr + (lane >> 2)) + quarter;
+                if (groups <= gr || r >= p.rows) break;
+                float* d = p.scores + (((long long)w.b * p.Hkv + w.h) * p.rows + r) * p.score_cap + k0 + 64 * half + 2 * cq;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(d + 8 * j) = make_uint2(S(gr, j, 0), S(gr, j, 1));
+              }
+            }
             // Scores are taken relative to a reference of the row, its
             // largest score when the reference was last set: it is set again,
             // and O rescaled, only when a score passes it by 2^kRaise. P and
@@ -426,43 +450,99 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       if (!ok) break;
       g += 2 * w.n;
-      // ---- the piece's partial result
+      // ---- the piece's result
       if (!(ok = wait(bar(B_OFINAL), n_piece & 1))) break;
-      ++n_piece;
       tc_fence_after();
-      const bool used = NQT == 2 || w.n > stream;     // a stream without tiles has no O
-      const long long slot = ((long long)blockIdx.x + w.item) * 2 + stream;
+      float sum[4];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (groups <= 2 * hf) break;
-        const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
-        float lA, lB, y;
-        unpk2(l[2 * hf], lA, y);
-        lA += y;
-        unpk2(l[2 * hf + 1], lB, y);
-        lB += y;
-        lA += __shfl_xor_sync(0xffffffffu, lA, 1);
-        lB += __shfl_xor_sync(0xffffffffu, lB, 1);
-        lA += __shfl_xor_sync(0xffffffffu, lA, 2);
-        lB += __shfl_xor_sync(0xffffffffu, lB, 2);
-        const int ra = 4 * (16 * hf + (lane >> 2)) + quarter, rb = ra + 32;     // rows within the tile
-        if (cq == 0) {
-          if (ra < srows) p.part_ml[slot * p.row_cap + ra] = make_float2(m[2 * hf], lA);
-          if (rb < srows) p.part_ml[slot * p.row_cap + rb] = make_float2(m[2 * hf + 1], lB);
+      for (int gr = 0; gr < 4; ++gr) {
+        float y;
+        unpk2(l[gr], sum[gr], y);
+        sum[gr] += y;
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+      }
+      // With one query tile both streams hold parts of the same rows, O in
+      // the same TMEM lanes: stream 1 hands over its references and sums, and
+      // stream 0 joins the two.
+      float f0[4], f1[4];
+      float2* xchg = reinterpret_cast<float2*>(smem + OFF_XCHG);
+      if (NQT == 1 && stream == 1) {
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr)
+          if (cq == 0) xchg[quarter * 32 + 8 * gr + (lane >> 2)] = make_float2(m[gr], sum[gr]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_XCHG + quarter));
+      } else if (NQT == 1) {
+        if (!(ok = wait(bar(B_XCHG + quarter), n_piece & 1))) break;
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          const float2 o = xchg[quarter * 32 + 8 * gr + (lane >> 2)];
+          const float top = fmaxf(m[gr], o.x);
+          f0[gr] = m[gr] == -INFINITY ? 0.f : fast_exp2((m[gr] - top) * c);
+          f1[gr] = o.x == -INFINITY ? 0.f : fast_exp2((o.x - top) * c);
+          m[gr] = top;
+          sum[gr] = sum[gr] * f0[gr] + o.y * f1[gr];
         }
-        if (used) {
-          float* oa = p.part_o + (slot * p.row_cap + ra) * kHeadDim + 2 * cq;
+      }
+      ++n_piece;
+      if (NQT == 2 || stream == 0) {
+        const long long out_row = ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T + srow0;
+        const long long slot = ((long long)blockIdx.x + w.item) * NQT + (NQT == 2 ? stream : 0);
+        const bool two = NQT == 1 && w.n > 1;      // stream 1 had a tile
 #pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (groups <= 2 * hf) break;
+          const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
+          const int ra = 4 * (16 * hf + (lane >> 2)) + quarter, rb = ra + 32;     // rows within the tile
+          // a complete item is normalised here, rows of missing tokens are not written
+          const bool wa = ra < srows && (!w.complete || (srow0 + ra) % p.T < w.draft);
+          const bool wb = rb < srows && (!w.complete || (srow0 + rb) % p.T < w.draft);
+          float ga = 1.f, gb = 1.f;
+          if (w.complete) {
+            ga = sum[2 * hf] > 0.f ? 1.f / sum[2 * hf] : 0.f;
+            gb = sum[2 * hf + 1] > 0.f ? 1.f / sum[2 * hf + 1] : 0.f;
+          }
+          if (cq == 0) {
+            auto keep = [&](int r, int gr) {
+              if (!w.complete) {
+                p.part_ml[slot * p.row_cap + r] = make_float2(m[gr], sum[gr]);
+              } else {
+                if (p.lse) p.lse[out_row + r] = m[gr] * p.scale + logf(sum[gr]);
+                if (p.row_stat) p.row_stat[out_row + r] = make_float2(m[gr], 1.f / sum[gr]);
+              }
+            };
+            if (wa) keep(ra, 2 * hf);
+            if (wb) keep(rb, 2 * hf + 1);
+          }
+          const float a0 = NQT == 1 ? f0[2 * hf] * ga : ga, b0 = NQT == 1 ? f0[2 * hf + 1] * gb : gb;
+          const float a1 = NQT == 1 ? f1[2 * hf] * ga : 0.f, b1 = NQT == 1 ? f1[2 * hf + 1] * gb : 0.f;
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t o[16];
+            uint32_t o[16], o1[16];
             tmem_ld_16x256b_x4(tOh + 32 * q, o);
+            if (two) tmem_ld_16x256b_x4(tOh + 128 + 32 * q, o1);
             tmem_wait_ld();
+            float v[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (ra < srows)
-                *reinterpret_cast<uint2*>(oa + 32 * q + 8 * j) = make_uint2(o[4 * j], o[4 * j + 1]);
-              if (rb < srows)
-                *reinterpret_cast<uint2*>(oa + 32 * kHeadDim + 32 * q + 8 * j) = make_uint2(o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 16; ++j) {
+              v[j] = __uint_as_float(o[j]) * ((j & 2) ? b0 : a0);
+              if (two) v[j] = fmaf(__uint_as_float(o1[j]), (j & 2) ? b1 : a1, v[j]);
+            }
+            if (w.complete) {
+              __nv_bfloat16* oa = p.O + (out_row + ra) * kHeadDim + 32 * q + 2 * cq;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (wa) *reinterpret_cast<uint32_t*>(oa + 8 * j) = pack_bf16x2(v[4 * j], v[4 * j + 1]);
+                if (wb) *reinterpret_cast<uint32_t*>(oa + 32 * kHeadDim + 8 * j) = pack_bf16x2(v[4 * j + 2], v[4 * j + 3]);
+              }
+            } else {
+              float* oa = p.part_o + (slot * p.row_cap + ra) * kHeadDim + 32 * q + 2 * cq;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (wa) *reinterpret_cast<float2*>(oa + 8 * j) = make_float2(v[4 * j], v[4 * j + 1]);
+                if (wb) *reinterpret_cast<float2*>(oa + 32 * kHeadDim + 8 * j) = make_float2(v[4 * j + 2], v[4 * j + 3]);
+              }
             }
           }
         }
@@ -484,96 +564,122 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of one row: O = sum_i f_i O_i / sum_i f_i l_i, f_i =
-// exp(scale (m_i - M)).
-// One block of 128 threads per row, one thread per element.
-__global__ void __launch_bounds__(kHeadDim) tree_combine_kernel(const TreeParams p) {
-  __shared__ float f[2 * kMaxGrid];
-  __shared__ long long at[2 * kMaxGrid];
-  __shared__ int count;
-  __shared__ float top, sum;
+// Joins the pieces of a row that several CTAs share: O = sum_i f_i O_i /
+// sum_i f_i l_i, f_i = exp(scale (m_i - M)). One block of four warps per row:
+// every warp weighs all pieces, adds every fourth one (16 bytes a lane), and
+// the four sums meet in shared memory.
+__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
+  __shared__ float f[4][kMaxGrid];
+  __shared__ int at[4][kMaxGrid];
+  __shared__ float4 acc[4][32];
   const int r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
-  const int b = bh / p.Hkv, h = bh % p.Hkv, t = r % p.T;
+  const int b = bh / p.Hkv, h = bh % p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
   const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-  if (t >= s.draft) return;
+  if (r % p.T >= s.draft) {
+    wait_for_predecessors();       // no kernel of the chain ends before the one it follows
+    return;
+  }
   const int wide = p.rows > BM ? 2 : 1;              // query tiles of a block
   const int block = r / (wide * BM), tile = r / BM % wide, tr = r % BM;
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    long long sum_all = 0, sum_before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int n = b0 + lane < p.B ? key_tiles(p, b0 + lane) : 0;
-      sum_all += __reduce_add_sync(0xffffffffu, n);
-      sum_before += __reduce_add_sync(0xffffffffu, b0 + lane < b ? n : 0);
-    }
-    const long long per = (long long)p.Hkv * p.blocks, total = per * sum_all;
-    const int nt = key_tiles(p, s);
-    const long long a = per * sum_before + ((long long)h * p.blocks + block) * nt, e = a + nt;
-    const int item = bh * p.blocks + block;
-    // the CTAs whose shares [total c / grid, total (c + 1) / grid) meet [a, e)
-    const int c0 = (int)(((a + 1) * p.grid + total - 1) / total) - 1, c1 = (int)((e * p.grid + total - 1) / total) - 1;
-    int n = 0;
-    float mx = -INFINITY;
-    for (int x0 = c0 * 2; x0 <= c1 * 2 + 1; x0 += 32) {
-      const int x = x0 + lane, c = x >> 1, stream = x & 1;
-      bool has = c <= c1 && total * c / p.grid < total * (c + 1) / p.grid && (wide == 1 || stream == tile);
-      const long long slot = ((long long)(c + item) * 2 + stream) * p.row_cap + tr;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (has) ml = p.part_ml[slot];
-      has = has && ml.x != -INFINITY;
-      const uint32_t v = __ballot_sync(0xffffffffu, has);
-      if (has) {
-        const int q = n + __popc(v & ((1u << lane) - 1));
-        f[q] = ml.x;
-        at[q] = slot;
-      }
-      n += __popc(v);
-      mx = fmaxf(mx, ml.x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    __syncwarp();
-    float l = 0.f;
-    for (int q = lane; q < n; q += 32) {
-      const float k = fast_exp2((f[q] - mx) * p.scale_log2);
-      l += k * p.part_ml[at[q]].y;
-      f[q] = k;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) {
-      count = n;
-      top = mx;
-      sum = l;
-    }
+  int sum_all = 0, sum_before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int n = b0 + lane < p.B ? line_len(p, b0 + lane) : 0;
+    sum_all += n;
+    sum_before += b0 + lane < b ? n : 0;
   }
+  const long long per = (long long)p.Hkv * p.blocks, total = per * __reduce_add_sync(0xffffffffu, sum_all);
+  const int nt = line_len(p, s);
+  const long long a = per * __reduce_add_sync(0xffffffffu, sum_before) + ((long long)h * p.blocks + block) * nt;
+  const int item = bh * p.blocks + block;
+  // the CTAs whose shares [total c / grid, total (c + 1) / grid) meet [a, a + nt)
+  const int c0 = (int)(((a + 1) * p.grid + total - 1) / total) - 1;
+  const int c1 = (int)(((a + nt) * p.grid + total - 1) / total) - 1;
+  wait_for_predecessors();
+  if (c0 == c1) return;                              // one CTA had the whole item and wrote its rows
+  int n = 0;
+  float mx = -INFINITY;
+  for (int x0 = c0; x0 <= c1; x0 += 32) {
+    const int c = x0 + lane;
+    const bool has = c <= c1 && total * c / p.grid < total * (c + 1) / p.grid;
+    const int slot = (c + item) * wide + tile;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (has) ml = p.part_ml[(long long)slot * p.row_cap + tr];
+    const uint32_t v = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+    if (ml.x != -INFINITY) {
+      const int q = n + __popc(v & ((1u << lane) - 1));
+      f[warp][q] = ml.x;
+      at[warp][q] = slot;
+    }
+    n += __popc(v);
+    mx = fmaxf(mx, ml.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  __syncwarp();
+  float l = 0.f;
+  for (int q = lane; q < n; q += 32) {
+    const float k = fast_exp2((f[warp][q] - mx) * p.scale_log2);
+    l += k * p.part_ml[(long long)at[warp][q] * p.row_cap + tr].y;
+    f[warp][q] = k;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  __syncwarp();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int q = warp; q < n; q += 4) {
+    const float k = f[warp][q];
+    const float4 v =
+        *reinterpret_cast<const float4*>(p.part_o + ((long long)at[warp][q] * p.row_cap + tr) * kHeadDim + 4 * lane);
+    o.x += k * v.x;
+    o.y += k * v.y;
+    o.z += k * v.z;
+    o.w += k * v.w;
+  }
+  acc[warp][lane] = o;
   __syncthreads();
-  float o = 0.f;
-  const int n = count;
-#pragma unroll 4
-  for (int q = 0; q < n; ++q) o += f[q] * p.part_o[at[q] * kHeadDim + threadIdx.x];
   const long long row = (long long)bh * p.rows + r;
-  p.O[row * kHeadDim + threadIdx.x] = __float2bfloat16(n ? o / sum : 0.f);
-  if (threadIdx.x == 0) {
-    if (p.lse) p.lse[row] = n ? top * p.scale + logf(sum) : -INFINITY;
-    if (p.row_stat) p.row_stat[row] = make_float2(top, 1.f / sum);
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      const float4 v = acc[i][lane];
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
+    }
+    const float g = l > 0.f ? 1.f / l : 0.f;
+    *reinterpret_cast<uint2*>(p.O + row * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16x2(o.x * g, o.y * g), pack_bf16x2(o.z * g, o.w * g));
+    if (lane == 0) {
+      if (p.lse) p.lse[row] = mx * p.scale + logf(l);
+      if (p.row_stat) p.row_stat[row] = make_float2(mx, 1.f / l);
+    }
   }
 }
 
 struct Plan {
-  int rows, wide, blocks, row_cap;
-  size_t o_bytes, ml_bytes, stat_bytes;
+  int rows, wide, blocks, row_cap, score_cap;
+  bool whole, scores;
+  size_t o_bytes, ml_bytes, stat_bytes, score_bytes;
 };
-Plan make_plan(int B, int Hq, int Hkv, int T, bool want_weight) {
+Plan make_plan(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
   Plan q;
   q.rows = Hq / Hkv * T;
   q.wide = q.rows > BM ? 2 : 1;
   q.blocks = ceil_div(q.rows, q.wide * BM);
   q.row_cap = q.rows < BM ? q.rows : BM;
-  const size_t pieces = (size_t)B * Hkv * q.blocks + kMaxGrid;
-  q.o_bytes = pieces * 2 * q.row_cap * kHeadDim * sizeof(float);   // a multiple of 512
-  q.ml_bytes = (pieces * 2 * q.row_cap * sizeof(float2) + 255) / 256 * 256;
-  q.stat_bytes = want_weight ? sizeof(float2) * (size_t)B * Hq * T : 0;
+  q.score_cap = ceil_div(cap, BN) * BN;
+  q.whole = cap <= kWholeTiles * BN;
+  q.scores = want_weight && q.rows <= kMaxScoreRows;
+  const size_t pieces = q.whole ? 0 : (size_t)B * Hkv * q.blocks + kMaxGrid;
+  auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+  q.o_bytes = round(pieces * q.wide * q.row_cap * kHeadDim * sizeof(float));
+  q.ml_bytes = round(pieces * q.wide * q.row_cap * sizeof(float2));
+  q.stat_bytes = want_weight ? round(sizeof(float2) * (size_t)B * Hq * T) : 0;
+  q.score_bytes = q.scores ? sizeof(float) * (size_t)B * Hkv * q.rows * q.score_cap : 0;
   return q;
 }
 
@@ -583,25 +689,25 @@ int tree_max_drafts() { return kMaxDrafts; }
 int tree_max_group() { return kMaxGroup; }
 
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
-  const Plan q = make_plan(B, Hq, Hkv, T, want_weight);
-  return q.o_bytes + q.ml_bytes + q.stat_bytes;
+  const Plan q = make_plan(B, Hq, Hkv, T, cap, want_weight);
+  return 256 + q.o_bytes + q.ml_bytes + q.stat_bytes + q.score_bytes;
 }
 
 int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const void* V, const RowStrides& vs, int B,
                      int Hq, int Hkv, int T, int cap, const int32_t* lengths, const int32_t* parents,
                      const int32_t* n_draft, float softmax_scale, void* O, float* lse, const float* weight,
                      float* weight_out, void* ws, unsigned int* status, cudaStream_t stream) {
-  const Plan q = make_plan(B, Hq, Hkv, T, weight_out != nullptr);
+  const Plan q = make_plan(B, Hq, Hkv, T, cap, weight_out != nullptr);
   EncodeTiledFn enc = tmap_encode_fn();
   if (!enc) return cuda_status(cudaErrorNotSupported);
   TreeMaps maps;
   if (!make_cache_map(enc, &maps.k, K, ks, B, Hkv, cap, BN) || !make_cache_map(enc, &maps.v, V, vs, B, Hkv, cap, BN))
     return DHSA_ERR_INVALID_ARG;
+  static bool done[2][64] = {{false}};
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = this_device(&dev, &sms);
   auto* kernel = q.wide == 2 ? tree_attn_kernel<2> : tree_attn_kernel<1>;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemAlloc);
+  if (e == cudaSuccess) e = allow_smem(kernel, (int)kSmemAlloc, dev, done[q.wide - 1]);
   if (e != cudaSuccess) return cuda_status(e);
 
   TreeParams p;
@@ -611,9 +717,13 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.n_draft = n_draft;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.lse = lse;
-  p.part_o = static_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + q.o_bytes);
-  p.row_stat = weight_out ? reinterpret_cast<float2*>(static_cast<char*>(ws) + q.o_bytes + q.ml_bytes) : nullptr;
+  char* at = static_cast<char*>(ws);
+  p.part_o = reinterpret_cast<float*>(at);
+  p.part_ml = reinterpret_cast<float2*>(at += q.o_bytes);
+  p.row_stat = reinterpret_cast<float2*>(at += q.ml_bytes);
+  p.scores = reinterpret_cast<float*>(at += q.stat_bytes);
+  if (!weight_out) p.row_stat = nullptr;
+  if (!q.scores) p.scores = nullptr;
   p.weight = weight;
   p.weight_out = weight_out;
   p.B = B;
@@ -627,16 +737,23 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.row_cap = q.row_cap;
   p.every = false;
   p.tile = BN;
-  const long long most = (long long)B * Hkv * q.blocks * ceil_div(cap, BN);   // tiles at full lengths
+  p.score_cap = q.score_cap;
+  p.whole = q.whole;
+  p.keep_k = weight_out && !q.scores;
+  const long long most = (long long)B * Hkv * q.blocks * (q.whole ? 1 : ceil_div(cap, BN));   // the line's length at most
   p.grid = sms < kMaxGrid ? sms : kMaxGrid;
   if (most < p.grid) p.grid = (int)most;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = status;
   kernel<<<p.grid, kThreads, kSmemAlloc, stream>>>(maps, p);
-  tree_combine_kernel<<<(unsigned)((long long)B * Hkv * q.rows), kHeadDim, 0, stream>>>(p);
   int st = launch_status();
-  if (st == DHSA_OK && weight_out) {
+  if (st == DHSA_OK && !q.whole)
+    st = launch_after(tree_combine_kernel, dim3((unsigned)((long long)B * Hkv * q.rows)), dim3(128), 0, stream, p);
+  if (st == DHSA_OK && weight_out && q.scores) {
+    st = launch_tree_weight_scores(p, stream);
+  } else if (st == DHSA_OK && weight_out) {
+    p.whole = false;
     p.every = true;                   // weights without new tokens are passed on
     p.blocks = 1;                     // one walk over the keys for all rows of a head
     p.tile = tree_weight_tile();

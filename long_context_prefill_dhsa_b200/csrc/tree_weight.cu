@@ -12,6 +12,8 @@
 // 256 columns, warps 4 to 7 take the even and warps 8 to 11 the odd tiles.
 // More than 256 rows walk the same keys again and add to weight_out.
 // Waits are bounded as in tree_attn.cu.
+#include <type_traits>
+
 #include "tree.cuh"
 
 namespace dhsa {
@@ -38,8 +40,8 @@ enum {
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_RING = 2 * kQHalfBytes;
 constexpr uint32_t OFF_STAT = OFF_RING + kStages * kTileBytes;     // float4 per pair of rows: -M0, -M1, 1/l0, 1/l1
-constexpr uint32_t OFF_SEE = OFF_STAT + kRowBlock / 2 * 16;        // per row: drafted tokens it sees
-constexpr uint32_t OFF_BAR = OFF_SEE + kRowBlock * 8;
+constexpr uint32_t OFF_SEE = OFF_STAT + kRowBlock / 2 * 16;        // per drafted token: those it sees
+constexpr uint32_t OFF_BAR = OFF_SEE + kMaxDrafts * 8;
 constexpr uint32_t OFF_LINE = OFF_BAR + 8 * ((W_COUNT + 1) & ~1);
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
@@ -97,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
     if (lane == 0) {
       uint32_t g = 0;
       bool ok = true;
+      const uint64_t usual = l2_evict_normal(), last = l2_evict_first();
       while (ok && walk.next(p, &w)) {
         for (int rb = 0; ok && rb < walks; ++rb)
           for (int i = 0; i < w.n; ++i, ++g) {
@@ -107,8 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
             }
             const uint32_t dst = sbase + OFF_RING + st * kTileBytes;
             mbar_arrive_expect_tx(bar(W_FULL + st), kTileBytes);
-            tma_load_4d(dst, &kmap, bar(W_FULL + st), 0, (w.t0 + i) * BN, w.h, w.b);
-            tma_load_4d(dst + kHalfBytes, &kmap, bar(W_FULL + st), 64, (w.t0 + i) * BN, w.h, w.b);
+            // the last walk over a tile needs it no longer
+            const uint64_t policy = rb == walks - 1 ? last : usual;
+            tma_load_4d(dst, &kmap, bar(W_FULL + st), 0, (w.t0 + i) * BN, w.h, w.b, policy);
+            tma_load_4d(dst + kHalfBytes, &kmap, bar(W_FULL + st), 64, (w.t0 + i) * BN, w.h, w.b, policy);
           }
       }
       for (uint32_t q = g > kStages ? g - kStages : 0; q < g; ++q)
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         for (int rb = 0; ok && rb < walks; ++rb) {
           if (!(ok = wait(bar(W_QREADY), n_q++ & 1))) break;
           const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock);
-          const uint32_t idesc = idesc_bf16_f32(BN, (n_rows + 15) & ~15, false);
+          const uint32_t idesc = idesc_bf16_f32(BN, (n_rows + 31) & ~31, false);
           for (int i = 0; i < w.n; ++i, ++g) {
             const int s = i & 1;
             const uint32_t st = g % kStages;
@@ -152,18 +157,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
     const uint64_t c2 = pk2(c, c);
     uint32_t n_s = 0, n_done = 0;
     bool ok = true;
+    wait_for_predecessors();       // the rows' statistics come from the attention
     while (ok && walk.next(p, &w)) {
       const long long row_base = ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T;
       const int slots = w.len + w.draft;
       const bool tail = (w.t0 + w.n) * BN > w.len;
       const float* w_in = p.weight + ((long long)w.b * p.Hkv + w.h) * p.cap;
       float* w_out = p.weight_out + ((long long)w.b * p.Hkv + w.h) * p.cap;
-      Sees sv{0, 0};
-      if (tail) sv = tree_sees(p, w.b, w.draft, lane);
+      if (tail) {      // the same values from every warp
+        const Sees sv = tree_sees(p, w.b, w.draft, lane);
+        see[lane] = sv.m0;
+        see[lane + 32] = sv.m1;
+      }
       for (int rb = 0; ok && rb < walks; ++rb) {
         // the Q operand and the row statistics: 32 rows per warp. Rows past
         // the end and of missing tokens are zeros with weight 0.
-        const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock), n_pad = (n_rows + 15) & ~15;
+        const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock), n_pad = (n_rows + 31) & ~31;
         const int ch = lane & 15;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {       // eight loads in flight
@@ -186,13 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         {
           const int at = (warp - 4) * 32 + lane, r = rb * kRowBlock + at;
           const int t = r % p.T;
-          const uint64_t sees = sv.of(t);
           float2 st = make_float2(0.f, 0.f);
           if (at < n_rows && t < w.draft) st = p.row_stat[row_base + r];
           float* f = reinterpret_cast<float*>(stat + at / 2);
           f[at & 1] = -st.x;
           f[2 + (at & 1)] = st.y;
-          see[at] = sees;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -208,38 +215,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
           if (!(ok = wait(bar(W_SFULL + buf), n_s & 1))) break;
           ++n_s;
           tc_fence_after();
-          const bool masked = (w.t0 + i + 1) * BN > w.len;
           const int d = slot - w.len;                // drafted token of the slot
-          uint64_t acc = 0ull;
-          float acc1 = 0.f;
-          for (int r0 = 0; r0 < n_pad; r0 += 16) {
-            uint32_t s[16];
-            tmem_ld16(tS + r0, s);
-            tmem_wait_ld();
-            if (!masked) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float4 st = stat[(r0 + e) / 2];
-                const uint64_t x = mul2(add2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pk2(st.x, st.y)), c2);
-                float x0, x1;
-                unpk2(x, x0, x1);
-                acc = fma2(pk2(fast_exp2(x0), fast_exp2(x1)), pk2(st.z, st.w), acc);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float* f = reinterpret_cast<const float*>(stat + (r0 + e) / 2);
-                if (d < 0 || ((see[r0 + e] >> (d & 63)) & 1))
-                  acc1 += fast_exp2((__uint_as_float(s[e]) + f[e & 1]) * c) * f[2 + (e & 1)];
-              }
-            }
+          // which tokens see this slot, and the token of the walk's first row
+          uint64_t seen = ~0ull;
+          const bool masked = (w.t0 + i + 1) * BN > w.len;
+          if (masked && d >= 0) {
+            seen = 0;
+            for (int t = 0; t < w.draft; ++t) seen |= ((see[t] >> (d & 63)) & 1) << t;
           }
+          int t = rb * kRowBlock % p.T;
+          uint64_t acc[2] = {0ull, 0ull};
+          // 32 rows: their p, weighed and added in pairs
+          auto add = [&](auto with_mask, const uint32_t (&s)[32], int r0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float4 st = stat[(r0 + e) / 2];
+              const uint64_t x = mul2(add2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pk2(st.x, st.y)), c2);
+              float x0, x1;
+              unpk2(x, x0, x1);
+              x0 = fast_exp2(x0);
+              x1 = fast_exp2(x1);
+              if (with_mask.value) {
+                x0 = (seen >> t) & 1 ? x0 : 0.f;
+                t = t + 1 == p.T ? 0 : t + 1;
+                x1 = (seen >> t) & 1 ? x1 : 0.f;
+                t = t + 1 == p.T ? 0 : t + 1;
+              }
+              acc[(e >> 1) & 1] = fma2(pk2(x0, x1), pk2(st.z, st.w), acc[(e >> 1) & 1]);
+            }
+          };
+          // the next 32 columns are on their way while these are added
+          auto add_all = [&](auto with_mask) {
+            uint32_t s0[32], s1[32];
+            tmem_ld32(tS, s0);
+            tmem_wait_ld();
+#pragma unroll 1
+            for (int r0 = 0; r0 < n_pad; r0 += 64) {
+              if (r0 + 32 < n_pad) tmem_ld32(tS + r0 + 32, s1);
+              add(with_mask, s0, r0);
+              if (r0 + 32 >= n_pad) break;
+              tmem_wait_ld();
+              if (r0 + 64 < n_pad) tmem_ld32(tS + r0 + 64, s0);
+              add(with_mask, s1, r0 + 32);
+              tmem_wait_ld();
+            }
+          };
+          if (masked) add_all(std::true_type{});
+          else add_all(std::false_type{});
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(W_SEMPTY + buf));
           float a0, a1;
-          unpk2(acc, a0, a1);
-          if (live) w_out[slot] = old + (a0 + a1 + acc1);
+          unpk2(add2(acc[0], acc[1]), a0, a1);
+          if (live) w_out[slot] = old + (a0 + a1);
         }
         if (!ok) break;
         // Q and the statistics may change once every warp is done with them
@@ -263,16 +291,64 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   tmem_dealloc(tmem, kTmemCols);
 }
 
+// The same from scores that the attention kept, for few rows: 8 bytes per slot
+// and row instead of K's 256, nothing to compute but the exponentials.
+constexpr int kSlotThreads = 256, kSlotsEach = 4;
+__global__ void __launch_bounds__(kSlotThreads) tree_weight_scores_kernel(const TreeParams p) {
+  __shared__ float2 stat[kMaxScoreRows];
+  const int parts = (p.cap + kSlotThreads * kSlotsEach - 1) / (kSlotThreads * kSlotsEach);
+  const int bh = blockIdx.x / parts, b = bh / p.Hkv, h = bh % p.Hkv;
+  const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
+  const int block0 = blockIdx.x % parts * (kSlotThreads * kSlotsEach), first = block0 + threadIdx.x;
+  if (block0 >= s.len + s.draft) {
+    wait_for_predecessors();       // no kernel of the chain ends before the one it follows
+    return;
+  }
+  float old[kSlotsEach];
+#pragma unroll
+  for (int k = 0; k < kSlotsEach; ++k) {
+    const int slot = first + k * kSlotThreads;
+    old[k] = slot < s.len ? p.weight[(long long)bh * p.cap + slot] : 0.f;
+  }
+  wait_for_predecessors();
+  if (threadIdx.x < p.rows) {
+    const bool live = threadIdx.x % p.T < s.draft;
+    stat[threadIdx.x] = live ? p.row_stat[((long long)b * p.Hq + h * p.G) * p.T + threadIdx.x] : make_float2(0.f, 0.f);
+  }
+  __syncthreads();
+  float sum[kSlotsEach] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < p.rows; ++r) {
+    const float2 st = stat[r];
+    if (st.y == 0.f) continue;       // a missing token's row
+    const float* row = p.scores + ((long long)bh * p.rows + r) * p.score_cap + first;
+#pragma unroll
+    for (int k = 0; k < kSlotsEach; ++k)
+      if (first + k * kSlotThreads < s.len + s.draft)
+        sum[k] += fast_exp2((row[k * kSlotThreads] - st.x) * p.scale_log2) * st.y;
+  }
+#pragma unroll
+  for (int k = 0; k < kSlotsEach; ++k) {
+    const int slot = first + k * kSlotThreads;
+    if (slot < s.len + s.draft) p.weight_out[(long long)bh * p.cap + slot] = old[k] + sum[k];
+  }
+}
+
 }  // namespace
 
 int tree_weight_tile() { return BN; }
 
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(tree_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemAlloc);
+  static bool done[64] = {false};
+  int dev = 0, sms = 0;
+  cudaError_t e = this_device(&dev, &sms);
+  if (e == cudaSuccess) e = allow_smem(tree_weight_kernel, (int)kSmemAlloc, dev, done);
   if (e != cudaSuccess) return cuda_status(e);
-  tree_weight_kernel<<<p.grid, kThreads, kSmemAlloc, stream>>>(k, p);
-  return launch_status();
+  return launch_after(tree_weight_kernel, dim3(p.grid), dim3(kThreads), kSmemAlloc, stream, k, p);
+}
+
+int launch_tree_weight_scores(const TreeParams& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)((long long)ceil_div(p.cap, kSlotThreads * kSlotsEach) * p.B * p.Hkv));
+  return launch_after(tree_weight_scores_kernel, grid, dim3(kSlotThreads), 0, stream, p);
 }
 
 }  // namespace dhsa

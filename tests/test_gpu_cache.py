@@ -568,3 +568,11 @@ def test_two_streams_with_their_own_workspaces(lib):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, sets[i][4]) for o in got[i])
+
+
+@needs_gpu
+def test_evict_more_slots_than_a_cluster_holds_keys_for(lib):
+    """A cache so long that the largest cluster ranks the rest of its slots from memory."""
+    rng = np.random.default_rng(33)
+    cap = 16 * 48 * 1024 + 7000
+    _check_evict(lib, rng, 1, 1, cap, [cap - 5], 900, n_draft=[5], accept=[0b10011], sinks=2, recent=5)
