@@ -19,14 +19,14 @@
 //   others leave an unnormalised O with its reference score and sum for each
 //   piece, and a second kernel joins an item's pieces.
 // * Two softmax streams per CTA, each with its own S and O in TMEM (4 x 128
-//   columns) and its own four warps. With up to 128 rows they take the even
+//   columns) and its own warps. With up to 128 rows they take the even
 //   and the odd key tiles of the same query tile; with more they take two
 //   query tiles over the same key tiles. While one stream does its
 //   exponentials the tensor core works for the other, and each half of P
 //   goes to the tensor core while the softmax does the other half.
 // * Warp 0 streams K and V tiles (TMA, 32 KB each) into one ring; warp 1
 //   issues S = Q K^T (both operands in shared memory) and O += P V (P from
-//   TMEM, over the S it came from); warps 4 to 11 are the streams' softmax.
+//   TMEM, over the S it came from); the warps from 4 on are the streams' softmax.
 //   A single issuer keeps the tensor operations in order.
 // * Query row r sits in TMEM lane 32 (r mod 4) + r / 4, so that few rows (one
 //   token: G of them) spread over all four lane quarters, and the shape
@@ -47,7 +47,8 @@ int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t s
 
 namespace {
 
-constexpr int kThreads = 384;
+// producer, issuer, two helpers, and the softmax: eight warps for each half of the lanes of a quarter in use
+constexpr int block_threads(int halves) { return 128 + 256 * halves; }
 constexpr int BM = 128;          // query rows per tile
 constexpr int BN = 128;          // slots per key tile
 constexpr uint32_t kHalfBytes = BM * 128;    // 128 query rows x 64 bf16, 128-byte swizzle
@@ -74,8 +75,8 @@ enum {
   B_PREADY = B_SFULL + 2,       // [stream][half]: P of 64 slots written
   B_PVHALF = B_PREADY + 4,      // per stream: P V of a tile's first half complete
   B_OFINAL = B_PVHALF + 2,      // every MMA of the piece complete
-  B_XCHG,                       // per lane quarter: stream 1's references and sums written
-  B_FINAL = B_XCHG + 4,
+  B_XCHG,                       // per lane quarter and half: stream 1's references and sums written
+  B_FINAL = B_XCHG + 8,
   B_TEARDOWN,
   B_COUNT
 };
@@ -91,9 +92,11 @@ static_assert(sizeof(Line) % 8 == 0, "alignment");
 
 constexpr int W_PRODUCER = 0, W_MMA = 1, W_SOFTMAX0 = 4;
 
-template <int NQT>   // query tiles per CTA
-__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ TreeMaps maps,
+// NQT: query tiles per CTA. HALVES: lane halves in use (one: up to 64 rows).
+template <int NQT, int HALVES>
+__global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(const __grid_constant__ TreeMaps maps,
                                                                 const TreeParams p) {
+  constexpr int kThreads = block_threads(HALVES), kStreamWarps = 4 * HALVES;
   constexpr int NST = (kSmemData - NQT * kTileBytes) / kKvBytes;   // ring stages
   constexpr int kAhead = 2 / NQT;   // tiles whose scores are computed ahead: one S for each of two streams
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -106,45 +109,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (warp == W_PRODUCER) {
-    if (lane == 0) {
-      *abort_flag = 0;
-      for (int s = 0; s < NST; ++s) {
-        mbar_init(bar(B_FULL + s), 1);
-        mbar_init(bar(B_EMPTY + s), 1);
-      }
-      mbar_init(bar(B_QREADY), 8);
-      for (int s = 0; s < 4; ++s) mbar_init(bar(B_PREADY + s), 4);
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(bar(B_SFULL + s), 1);
-        mbar_init(bar(B_PVHALF + s), 1);
-      }
-      mbar_init(bar(B_OFINAL), 1);
-      for (int s = 0; s < 4; ++s) mbar_init(bar(B_XCHG + s), 1);
-      mbar_init(bar(B_FINAL), 1);
-      mbar_init(bar(B_TEARDOWN), kThreads / 32 - 1);
-      fence_mbar_init();
-      prefetch_tmap(&maps.k);
-      prefetch_tmap(&maps.v);
+  if (warp == W_PRODUCER && lane == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(B_FULL + s), 1);
+      mbar_init(bar(B_EMPTY + s), 1);
     }
-  } else if (warp == W_MMA) {
-    tmem_alloc(sbase + OFF_TMEMPTR, kTmemCols);
-    tmem_relinquish();
-  } else if (warp == 2) {
-    const Line L = find_share(p, blockIdx.x, lane);
-    if (lane == 0) *line = L;
-  } else if (warp == 3 && blockIdx.x == 0) {
-    bool bad = false;
-    for (int b = lane; b < p.B; b += 32) bad |= seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap).bad;
-    if (bad) raise_device_flag(p.status, DHSA_DEVFLAG_BAD_CACHE);
+    mbar_init(bar(B_QREADY), 2 * kStreamWarps);
+    for (int s = 0; s < 4; ++s) mbar_init(bar(B_PREADY + s), kStreamWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(B_SFULL + s), 1);
+      mbar_init(bar(B_PVHALF + s), 1);
+    }
+    mbar_init(bar(B_OFINAL), 1);
+    for (int s = 0; s < 8; ++s) mbar_init(bar(B_XCHG + s), 1);
+    mbar_init(bar(B_FINAL), 1);
+    mbar_init(bar(B_TEARDOWN), kThreads / 32 - 1);
+    fence_mbar_init();
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   launch_dependents();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR);
+  // The producer needs nothing but the barriers and its share: it starts the
+  // copies while the others allocate TMEM and look up theirs.
+  Line share;
+  uint32_t tmem = 0;
+  if (warp == W_PRODUCER) {
+    share = find_share(p, blockIdx.x, lane);
+  } else {
+    if (warp == W_MMA) {
+      tmem_alloc(sbase + OFF_TMEMPTR, kTmemCols);
+      tmem_relinquish();
+    } else if (warp == 2) {
+      share = find_share(p, blockIdx.x, lane);
+      if (lane == 0) *line = share;
+    } else if (warp == 3 && blockIdx.x == 0) {
+      bool bad = false;
+      for (int b = lane; b < p.B; b += 32) bad |= seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap).bad;
+      if (bad) raise_device_flag(p.status, DHSA_DEVFLAG_BAD_CACHE);
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
+    tc_fence_after();
+    tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR);
+    share = *line;
+  }
   const Waits wait{abort_flag, p.status};
-  Pieces walk{line->start, line->end, line->base, line->b};
+  Pieces walk{share.start, share.end, share.base, share.b};
   Piece w{};
 
   if (warp == W_PRODUCER) {
@@ -178,78 +188,84 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       for (uint32_t q = g > NST ? g - NST : 0; q < g; ++q) mbar_wait(bar(B_FULL + q % NST), (q / NST) & 1, kWaitLimitNs);
     }
   } else if (warp == W_MMA) {
-    if (lane == 0) {
-      const uint32_t idesc_qk = idesc_bf16_f32(BM, BN, false), idesc_pv = idesc_bf16_f32(BM, kHeadDim, true);
-      uint32_t g = 0, n_piece = 0, p_phase = 0;    // p_phase: parity of P's barriers, a bit for each stream
-      auto qk = [&](int s, uint32_t stage) {      // S = Q K^T
-        const uint32_t qa = sbase + (NQT == 2 ? s * kTileBytes : 0), ka = ring + stage * kKvBytes;
+    // The whole warp runs the loop converged and lane 0 issues.
+    const uint32_t on = lane == 0;
+    const uint32_t idesc_qk = idesc_bf16_f32(BM, BN, false), idesc_pv = idesc_bf16_f32(BM, kHeadDim, true);
+    constexpr uint32_t kHi = desc_hi_sw128(1024);
+    const uint32_t q_lo = desc_lo_sw128(sbase, 16), k_lo = desc_lo_sw128(ring, 16);
+    const uint32_t v_lo = desc_lo_sw128(ring, kKvHalfBytes);
+    uint32_t g = 0, n_piece = 0, p_phase = 0;    // p_phase: parity of P's barriers, a bit for each stream
+    auto qk = [&](int s, uint32_t stage) {      // S = Q K^T
+      const uint32_t qa = q_lo + (NQT == 2 ? s * (kTileBytes >> 4) : 0), ka = k_lo + stage * (kKvBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + s * 128, smem_desc_sw128(qa + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024),
-                 smem_desc_sw128(ka + (k >> 2) * kKvHalfBytes + (k & 3) * 32, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
-        mma_commit(bar(B_SFULL + s));
-      };
-      auto arrived = [&](uint32_t q) {
-        const bool ok = wait(bar(B_FULL + q % NST), (q / NST) & 1);
+      for (int k = 0; k < 8; ++k)
+        mma_ss_lo(on, tmem + s * 128, qa + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+                  ka + (((k >> 2) * kKvHalfBytes + (k & 3) * 32) >> 4), kHi, idesc_qk, k > 0 ? 1u : 0u);
+      mma_commit_on(on, bar(B_SFULL + s));
+    };
+    auto arrived = [&](uint32_t q) {
+      const bool ok = wait(bar(B_FULL + q % NST), (q / NST) & 1);
+      tc_fence_after();
+      return ok;
+    };
+    auto pv = [&](int s, uint32_t q, bool first) {      // O += P V, each half as soon as its P is there
+      const uint32_t va = v_lo + (q % NST) * (kKvBytes >> 4);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait(bar(B_PREADY + 2 * s + half), (p_phase >> s) & 1)) return false;
+        if (half == 0 && !wait(bar(B_FULL + q % NST), (q / NST) & 1)) return false;
         tc_fence_after();
-        return ok;
-      };
-      auto pv = [&](int s, uint32_t q, bool first) {      // O += P V, each half as soon as its P is there
-        const uint32_t va = ring + (q % NST) * kKvBytes;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait(bar(B_PREADY + 2 * s + half), (p_phase >> s) & 1)) return false;
-          if (half == 0 && !wait(bar(B_FULL + q % NST), (q / NST) & 1)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; ++k)
-            mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, smem_desc_sw128(va + k * 2048, kKvHalfBytes, 1024),
-                   idesc_pv, (!first || k > 0) ? 1u : 0u);
-          if (half == 0) mma_commit(bar(B_PVHALF + s));
-        }
-        p_phase ^= 1u << s;
-        return true;
-      };
-      bool ok = true;
-      while (ok && walk.next(p, &w)) {
-        if (!wait(bar(B_QREADY), n_piece & 1)) break;
-        tc_fence_after();
-        for (int i = 0; i < kAhead && i < w.n; ++i) {
-          if (!(ok = arrived(g))) break;
-          qk(NQT == 1 ? i : 0, g % NST);
-          if (NQT == 2) qk(1, g % NST);
-          mma_commit(bar(B_EMPTY + g++ % NST));
-        }
-        for (int i = 0; ok && i < w.n; ++i) {
-          const bool more = i + kAhead < w.n;
-          const uint32_t gv = g++, gk = more ? g++ : 0;
-          if (!(ok = pv(NQT == 1 ? i & 1 : 0, gv, i < kAhead))) break;
-          if (NQT == 1) mma_commit(bar(B_EMPTY + gv % NST));
-          if (more) {
-            if (!(ok = arrived(gk))) break;
-            qk(NQT == 1 ? i & 1 : 0, gk % NST);
-            if (NQT == 1) mma_commit(bar(B_EMPTY + gk % NST));
-          }
-          if (NQT == 2) {
-            if (!(ok = pv(1, gv, i == 0))) break;
-            mma_commit(bar(B_EMPTY + gv % NST));
-            if (more) {
-              qk(1, gk % NST);
-              mma_commit(bar(B_EMPTY + gk % NST));
-            }
-          }
-        }
-        if (!ok) break;
-        mma_commit(bar(B_OFINAL));
-        ++n_piece;
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
+          mma_ts_lo(on, tmem + 256 + s * 128, tmem + s * 128 + k * 8, va + k * (2048 >> 4), kHi, idesc_pv,
+                    (!first || k > 0) ? 1u : 0u);
+        if (half == 0) mma_commit_on(on, bar(B_PVHALF + s));
       }
-      mma_commit(bar(B_FINAL));
-      mbar_wait(bar(B_FINAL), 0, kWaitLimitNs);
+      p_phase ^= 1u << s;
+      return true;
+    };
+    bool ok = true;
+    while (ok && walk.next(p, &w)) {
+      if (!wait(bar(B_QREADY), n_piece & 1)) break;
+      tc_fence_after();
+      for (int i = 0; i < kAhead && i < w.n; ++i) {
+        if (!(ok = arrived(g))) break;
+        qk(NQT == 1 ? i : 0, g % NST);
+        if (NQT == 2) qk(1, g % NST);
+        mma_commit_on(on, bar(B_EMPTY + g++ % NST));
+      }
+      for (int i = 0; ok && i < w.n; ++i) {
+        const bool more = i + kAhead < w.n;
+        const uint32_t gv = g++, gk = more ? g++ : 0;
+        if (!(ok = pv(NQT == 1 ? i & 1 : 0, gv, i < kAhead))) break;
+        if (NQT == 1) mma_commit_on(on, bar(B_EMPTY + gv % NST));
+        if (more) {
+          if (!(ok = arrived(gk))) break;
+          qk(NQT == 1 ? i & 1 : 0, gk % NST);
+          if (NQT == 1) mma_commit_on(on, bar(B_EMPTY + gk % NST));
+        }
+        if (NQT == 2) {
+          if (!(ok = pv(1, gv, i == 0))) break;
+          mma_commit_on(on, bar(B_EMPTY + gv % NST));
+          if (more) {
+            qk(1, gk % NST);
+            mma_commit_on(on, bar(B_EMPTY + gk % NST));
+          }
+        }
+      }
+      if (!ok) break;
+      mma_commit_on(on, bar(B_OFINAL));
+      ++n_piece;
     }
+    __syncwarp();
+    mma_commit_on(on, bar(B_FINAL));
+    mbar_wait(bar(B_FINAL), 0, kWaitLimitNs);
   } else if (warp >= W_SOFTMAX0) {
-    const int stream = (warp - W_SOFTMAX0) >> 2, quarter = warp & 3;
+    // a stream's warps: HALVES for each lane quarter, 16 lanes each
+    const int stream = (warp - W_SOFTMAX0) / kStreamWarps, quarter = warp & 3;
+    const int hf = HALVES == 2 ? ((warp - W_SOFTMAX0) >> 2) & 1 : 0;
     const int cq = lane & 3;
-    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + stream * 128;
+    const uint32_t tS = tmem + ((uint32_t)(quarter * 32 + hf * 16) << 16) + stream * 128;
     const uint32_t tO = tS + 256;
     const float c = p.scale_log2, raise = kRaise / c;
     const uint64_t c2 = pk2(c, c);
@@ -258,36 +274,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     uint32_t g = 0, n_t = 0, n_piece = 0;   // ring tiles and this stream's tiles used so far, pieces
     bool ok = true;
     while (ok && walk.next(p, &w)) {
-      // ---- the query tiles: eight warps, 16 (32) shared-memory rows each
+      // ---- the query tiles: each warp loads an equal share of the shared-memory rows
       const __nv_bfloat16* q_head = p.Q + ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T * kHeadDim;
       const int row0 = w.block * (NQT == 2 ? 2 * BM : BM);      // first row of the block
       const int ch = lane & 15;
+      constexpr int kEach = NQT * BM / (2 * kStreamWarps) / 2;   // 16-byte words of a lane
+      uint4 v[kEach];
 #pragma unroll
-      for (int part = 0; part < NQT; ++part) {      // eight loads in flight
-        uint4 v[8];
+      for (int it = 0; it < kEach; ++it) {
+        const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & 127;
+        const int r = row0 + (at >> 7) * BM + 4 * (L & 31) + (L >> 5);
+        v[it] = make_uint4(0, 0, 0, 0);
+        if (r < p.rows) v[it] = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
+      }
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int L = (warp - W_SOFTMAX0) * 16 + it * 2 + (lane >> 4);     // shared-memory row of the tile
-          const int r = row0 + part * BM + 4 * (L & 31) + (L >> 5);
-          v[it] = make_uint4(0, 0, 0, 0);
-          if (r < p.rows) v[it] = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
-        }
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int L = (warp - W_SOFTMAX0) * 16 + it * 2 + (lane >> 4);
-          *reinterpret_cast<uint4*>(smem + part * kTileBytes + (ch >> 3) * kHalfBytes + L * 128 +
-                                    (((ch & 7) ^ (L & 7)) << 4)) = v[it];
-        }
+      for (int it = 0; it < kEach; ++it) {
+        const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & 127;
+        *reinterpret_cast<uint4*>(smem + (at >> 7) * kTileBytes + (ch >> 3) * kHalfBytes + L * 128 +
+                                  (((ch & 7) ^ (L & 7)) << 4)) = v[it];
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_QREADY));
 
-      // ---- this thread's rows: lane quarter, two halves of 16 lanes, rows A (lane / 4) and B (+ 8)
+      // ---- this thread's rows: of the warp's 16 lanes, A (lane / 4) and B (+ 8)
       const int srow0 = row0 + (NQT == 2 ? stream * BM : 0);    // first row of this stream's tile
       const int srows = min(p.rows - srow0, BM);                // valid rows of it (can be <= 0)
       const int in_q = srows > quarter ? (srows - quarter + 3) >> 2 : 0;   // of this quarter
-      const int groups = (in_q + 7) >> 3;                       // of eight rows
+      const int groups = min(max(((in_q + 7) >> 3) - 2 * hf, 0), 2);      // of eight rows, this warp's
+      const int rowA = 4 * (16 * hf + (lane >> 2)) + quarter, rowB = rowA + 32;     // within the tile
       const int tail0 = w.len / BN;                             // first tile with drafted or empty slots
       const bool tail = w.t0 + w.n > tail0;
       if (tail) {
@@ -296,12 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         see[lane + 32] = sv.m1;
         __syncwarp();
       }
-      // per group of eight rows (A and B of the first half of the lanes, then
-      // of the second): reference score, two partial sums
-      float m[4];
-      uint64_t l[4];
+      // per row: reference score, two partial sums
+      float m[2];
+      uint64_t l[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         m[k] = -INFINITY;
         l[k] = 0ull;
       }
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           const uint32_t q = g + 2 * w.n - 1;      // the item's last tile is the piece's last load
           if (!(ok = wait(bar(B_FULL + q % NST), (q / NST) & 1))) break;
           unsigned char* v = smem + NQT * kTileBytes + (q % NST) * kKvBytes;
-          for (int x = (slots - k0) * 16 + quarter * 32 + lane; x < BN * 16; x += 128)
+          for (int x = (slots - k0) * 16 + (hf * 4 + quarter) * 32 + lane; x < BN * 16; x += 32 * kStreamWarps)
             *reinterpret_cast<uint4*>(v + (x & 1) * kKvHalfBytes + (x >> 1) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
@@ -325,18 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         for (int half = 0; half < 2; ++half) {
           if (groups > 0) {
             const uint32_t tSh = tS + half * 64, tP = tS + half * 32;
-            // s[32 hf + 4j + e]: row A of lane half hf, slot k0 + 64 half + 8j + 2cq + e; + 2: row B
-            uint32_t s[64];
-            tmem_ld_16x256b_x8(tSh, *reinterpret_cast<uint32_t(*)[32]>(s));
-            if (groups > 2) tmem_ld_16x256b_x8(tSh + (16u << 16), *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            // s[4j + e]: row A, slot k0 + 64 half + 8j + 2cq + e; s[4j + 2 + e]: row B
+            uint32_t s[32];
+            tmem_ld_16x256b_x8(tSh, s);
             tmem_wait_ld();
-            auto S = [&](int gr, int j, int e) -> uint32_t& { return s[32 * (gr >> 1) + 4 * j + 2 * (gr & 1) + e]; };
+            auto S = [&](int gr, int j, int e) -> uint32_t& { return s[4 * j + 2 * gr + e]; };
             const int n0 = w.len - k0 - 64 * half;      // slots of the half that hold cached keys
             if (n0 < 64) {
 #pragma unroll
-              for (int gr = 0; gr < 4; ++gr) {
-                if (groups <= gr) break;
-                const uint64_t sees = see[(srow0 + 4 * (8 * gr + (lane >> 2)) + quarter) % p.T];
+              for (int gr = 0; gr < 2; ++gr) {
+                const uint64_t sees = see[(srow0 + rowA + 32 * gr) % p.T];
                 uint64_t vis = n0 > 0 ? (sees << n0) | ((1ull << n0) - 1) : n0 > -64 ? sees >> -n0 : 0ull;
                 vis >>= 2 * cq;
 #pragma unroll
@@ -348,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             }
             if (NQT == 1 && p.scores) {      // for the weight pass
 #pragma unroll
-              for (int gr = 0; gr < 4; ++gr) {
-                const int r = 4 * (8 * gr + (lane >> 2)) + quarter;
-                if (groups <= gr || r >= p.rows) break;
+              for (int gr = 0; gr < 2; ++gr) {
+                const int r = rowA + 32 * gr;
+                if (r >= p.rows) break;
                 float* d = p.scores + (((long long)w.b * p.Hkv + w.h) * p.rows + r) * p.score_cap + k0 + 64 * half + 2 * cq;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(d + 8 * j) = make_uint2(S(gr, j, 0), S(gr, j, 1));
@@ -361,10 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             // and O rescaled, only when a score passes it by 2^kRaise. P and
             // the sums have fp32's exponent range, so O / l is the same; the
             // test needs no exchange between the row's threads.
-            float x[4];
+            float x[2];
             bool up = false;
 #pragma unroll
-            for (int gr = 0; gr < 4; ++gr) {
+            for (int gr = 0; gr < 2; ++gr) {
               x[gr] = -INFINITY;
               if (groups <= gr) continue;
               auto F = [&](int j, int e) { return __uint_as_float(S(gr, j, e)); };
@@ -378,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
               up = up || x[gr] > m[gr] + raise;
             }
             if (__any_sync(0xffffffffu, up)) {
-              float f[4];
+              float f[2];
 #pragma unroll
-              for (int gr = 0; gr < 4; ++gr) {
+              for (int gr = 0; gr < 2; ++gr) {
                 x[gr] = fmaxf(x[gr], __shfl_xor_sync(0xffffffffu, x[gr], 1));
                 x[gr] = fmaxf(x[gr], __shfl_xor_sync(0xffffffffu, x[gr], 2));
                 const bool r = x[gr] > m[gr] + raise;
@@ -392,20 +404,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
               if (half == 1 && !(ok = wait(bar(B_PVHALF + stream), n_t & 1))) break;
               tc_fence_after();
               if (i >= step || half == 1) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                  if (groups <= 2 * hf) break;
-                  const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
 #pragma unroll 1
-                  for (int q = 0; q < 4; ++q) {
-                    uint32_t o[16];
-                    tmem_ld_16x256b_x4(tOh + 32 * q, o);
-                    tmem_wait_ld();
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t o[16];
+                  tmem_ld_16x256b_x4(tO + 32 * q, o);
+                  tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                      o[j] = __float_as_uint(__uint_as_float(o[j]) * f[2 * hf + ((j >> 1) & 1)]);
-                    tmem_st_16x256b_x4(tOh + 32 * q, o);
-                  }
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+                  tmem_st_16x256b_x4(tO + 32 * q, o);
                 }
                 tmem_wait_st();
               }
@@ -413,33 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             // The difference is taken before the scale: scores near the
             // reference keep their distance to it exactly, however large they
             // are. A row that has seen nothing yet keeps m = -inf: its p are 0.
+            // pk[2j]: row A, pk[2j + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
+            uint32_t pk[16];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if (groups <= 2 * hf) break;
-              // pk[2j]: row A, pk[2j + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
-              uint32_t pk[16];
+            for (int gr = 0; gr < 2; ++gr) {
+              if (groups > gr) {
+                const float n = m[gr] == -INFINITY ? 0.f : -m[gr];
+                const uint64_t n2 = pk2(n, n);
 #pragma unroll
-              for (int ab = 0; ab < 2; ++ab) {
-                const int gr = 2 * hf + ab;
-                if (groups > gr) {
-                  const float n = m[gr] == -INFINITY ? 0.f : -m[gr];
-                  const uint64_t n2 = pk2(n, n);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    float x0, x1;
-                    unpk2(mul2(add2(pk2(__uint_as_float(S(gr, j, 0)), __uint_as_float(S(gr, j, 1))), n2), c2), x0, x1);
-                    x0 = fast_exp2(x0);
-                    x1 = fast_exp2(x1);
-                    l[gr] = add2(l[gr], pk2(x0, x1));
-                    pk[2 * j + ab] = pack_bf16x2(x0, x1);
-                  }
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) pk[2 * j + ab] = 0u;
+                for (int j = 0; j < 8; ++j) {
+                  float x0, x1;
+                  unpk2(mul2(add2(pk2(__uint_as_float(S(gr, j, 0)), __uint_as_float(S(gr, j, 1))), n2), c2), x0, x1);
+                  x0 = fast_exp2(x0);
+                  x1 = fast_exp2(x1);
+                  l[gr] = add2(l[gr], pk2(x0, x1));
+                  pk[2 * j + gr] = pack_bf16x2(x0, x1);
                 }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) pk[2 * j + gr] = 0u;
               }
-              tmem_st_16x128b_x8(tP + ((uint32_t)(16 * hf) << 16), pk);
             }
+            tmem_st_16x128b_x8(tP, pk);
             tmem_wait_st();
           }
           tc_fence_before();
@@ -453,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       // ---- the piece's result
       if (!(ok = wait(bar(B_OFINAL), n_piece & 1))) break;
       tc_fence_after();
-      float sum[4];
+      float sum[2];
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
+      for (int gr = 0; gr < 2; ++gr) {
         float y;
         unpk2(l[gr], sum[gr], y);
         sum[gr] += y;
@@ -465,19 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       // With one query tile both streams hold parts of the same rows, O in
       // the same TMEM lanes: stream 1 hands over its references and sums, and
       // stream 0 joins the two.
-      float f0[4], f1[4];
-      float2* xchg = reinterpret_cast<float2*>(smem + OFF_XCHG);
+      float f0[2], f1[2];
+      float2* xchg = reinterpret_cast<float2*>(smem + OFF_XCHG) + quarter * 32 + 16 * hf + (lane >> 2);
       if (NQT == 1 && stream == 1) {
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr)
-          if (cq == 0) xchg[quarter * 32 + 8 * gr + (lane >> 2)] = make_float2(m[gr], sum[gr]);
+        for (int gr = 0; gr < 2; ++gr)
+          if (cq == 0) xchg[8 * gr] = make_float2(m[gr], sum[gr]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_XCHG + quarter));
+        if (lane == 0) mbar_arrive(bar(B_XCHG + 2 * quarter + hf));
       } else if (NQT == 1) {
-        if (!(ok = wait(bar(B_XCHG + quarter), n_piece & 1))) break;
+        if (!(ok = wait(bar(B_XCHG + 2 * quarter + hf), n_piece & 1))) break;
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          const float2 o = xchg[quarter * 32 + 8 * gr + (lane >> 2)];
+        for (int gr = 0; gr < 2; ++gr) {
+          const float2 o = xchg[8 * gr];
           const float top = fmaxf(m[gr], o.x);
           f0[gr] = m[gr] == -INFINITY ? 0.f : fast_exp2((m[gr] - top) * c);
           f1[gr] = o.x == -INFINITY ? 0.f : fast_exp2((o.x - top) * c);
@@ -486,63 +487,57 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
       }
       ++n_piece;
-      if (NQT == 2 || stream == 0) {
+      if ((NQT == 2 || stream == 0) && groups > 0) {
         const long long out_row = ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T + srow0;
         const long long slot = ((long long)blockIdx.x + w.item) * NQT + (NQT == 2 ? stream : 0);
         const bool two = NQT == 1 && w.n > 1;      // stream 1 had a tile
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (groups <= 2 * hf) break;
-          const uint32_t tOh = tO + ((uint32_t)(16 * hf) << 16);
-          const int ra = 4 * (16 * hf + (lane >> 2)) + quarter, rb = ra + 32;     // rows within the tile
-          // a complete item is normalised here, rows of missing tokens are not written
-          const bool wa = ra < srows && (!w.complete || (srow0 + ra) % p.T < w.draft);
-          const bool wb = rb < srows && (!w.complete || (srow0 + rb) % p.T < w.draft);
-          float ga = 1.f, gb = 1.f;
-          if (w.complete) {
-            ga = sum[2 * hf] > 0.f ? 1.f / sum[2 * hf] : 0.f;
-            gb = sum[2 * hf + 1] > 0.f ? 1.f / sum[2 * hf + 1] : 0.f;
-          }
-          if (cq == 0) {
-            auto keep = [&](int r, int gr) {
-              if (!w.complete) {
-                p.part_ml[slot * p.row_cap + r] = make_float2(m[gr], sum[gr]);
-              } else {
-                if (p.lse) p.lse[out_row + r] = m[gr] * p.scale + logf(sum[gr]);
-                if (p.row_stat) p.row_stat[out_row + r] = make_float2(m[gr], 1.f / sum[gr]);
-              }
-            };
-            if (wa) keep(ra, 2 * hf);
-            if (wb) keep(rb, 2 * hf + 1);
-          }
-          const float a0 = NQT == 1 ? f0[2 * hf] * ga : ga, b0 = NQT == 1 ? f0[2 * hf + 1] * gb : gb;
-          const float a1 = NQT == 1 ? f1[2 * hf] * ga : 0.f, b1 = NQT == 1 ? f1[2 * hf + 1] * gb : 0.f;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[16], o1[16];
-            tmem_ld_16x256b_x4(tOh + 32 * q, o);
-            if (two) tmem_ld_16x256b_x4(tOh + 128 + 32 * q, o1);
-            tmem_wait_ld();
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              v[j] = __uint_as_float(o[j]) * ((j & 2) ? b0 : a0);
-              if (two) v[j] = fmaf(__uint_as_float(o1[j]), (j & 2) ? b1 : a1, v[j]);
-            }
-            if (w.complete) {
-              __nv_bfloat16* oa = p.O + (out_row + ra) * kHeadDim + 32 * q + 2 * cq;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (wa) *reinterpret_cast<uint32_t*>(oa + 8 * j) = pack_bf16x2(v[4 * j], v[4 * j + 1]);
-                if (wb) *reinterpret_cast<uint32_t*>(oa + 32 * kHeadDim + 8 * j) = pack_bf16x2(v[4 * j + 2], v[4 * j + 3]);
-              }
+        // a complete item is normalised here, rows of missing tokens are not written
+        const bool wa = rowA < srows && (!w.complete || (srow0 + rowA) % p.T < w.draft);
+        const bool wb = rowB < srows && (!w.complete || (srow0 + rowB) % p.T < w.draft);
+        float ga = 1.f, gb = 1.f;
+        if (w.complete) {
+          ga = sum[0] > 0.f ? 1.f / sum[0] : 0.f;
+          gb = sum[1] > 0.f ? 1.f / sum[1] : 0.f;
+        }
+        if (cq == 0) {
+          auto keep = [&](int r, int gr) {
+            if (!w.complete) {
+              p.part_ml[slot * p.row_cap + r] = make_float2(m[gr], sum[gr]);
             } else {
-              float* oa = p.part_o + (slot * p.row_cap + ra) * kHeadDim + 32 * q + 2 * cq;
+              if (p.lse) p.lse[out_row + r] = m[gr] * p.scale + logf(sum[gr]);
+              if (p.row_stat) p.row_stat[out_row + r] = make_float2(m[gr], 1.f / sum[gr]);
+            }
+          };
+          if (wa) keep(rowA, 0);
+          if (wb) keep(rowB, 1);
+        }
+        const float a0 = NQT == 1 ? f0[0] * ga : ga, b0 = NQT == 1 ? f0[1] * gb : gb;
+        const float a1 = NQT == 1 ? f1[0] * ga : 0.f, b1 = NQT == 1 ? f1[1] * gb : 0.f;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[16], o1[16];
+          tmem_ld_16x256b_x4(tO + 32 * q, o);
+          if (two) tmem_ld_16x256b_x4(tO + 128 + 32 * q, o1);
+          tmem_wait_ld();
+          float v[16];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (wa) *reinterpret_cast<float2*>(oa + 8 * j) = make_float2(v[4 * j], v[4 * j + 1]);
-                if (wb) *reinterpret_cast<float2*>(oa + 32 * kHeadDim + 8 * j) = make_float2(v[4 * j + 2], v[4 * j + 3]);
-              }
+          for (int j = 0; j < 16; ++j) {
+            v[j] = __uint_as_float(o[j]) * ((j & 2) ? b0 : a0);
+            if (two) v[j] = fmaf(__uint_as_float(o1[j]), (j & 2) ? b1 : a1, v[j]);
+          }
+          if (w.complete) {
+            __nv_bfloat16* oa = p.O + (out_row + rowA) * kHeadDim + 32 * q + 2 * cq;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (wa) *reinterpret_cast<uint32_t*>(oa + 8 * j) = pack_bf16x2(v[4 * j], v[4 * j + 1]);
+              if (wb) *reinterpret_cast<uint32_t*>(oa + 32 * kHeadDim + 8 * j) = pack_bf16x2(v[4 * j + 2], v[4 * j + 3]);
+            }
+          } else {
+            float* oa = p.part_o + (slot * p.row_cap + rowA) * kHeadDim + 32 * q + 2 * cq;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (wa) *reinterpret_cast<float2*>(oa + 8 * j) = make_float2(v[4 * j], v[4 * j + 1]);
+              if (wb) *reinterpret_cast<float2*>(oa + 32 * kHeadDim + 8 * j) = make_float2(v[4 * j + 2], v[4 * j + 3]);
             }
           }
         }
@@ -565,22 +560,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 }
 
 // Joins the pieces of a row that several CTAs share: O = sum_i f_i O_i /
-// sum_i f_i l_i, f_i = exp(scale (m_i - M)). One block of four warps per row:
-// every warp weighs all pieces, adds every fourth one (16 bytes a lane), and
-// the four sums meet in shared memory.
-__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
-  __shared__ float f[4][kMaxGrid];
-  __shared__ int at[4][kMaxGrid];
-  __shared__ float4 acc[4][32];
-  const int r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
-  const int b = bh / p.Hkv, h = bh % p.Hkv;
+// sum_i f_i l_i, f_i = exp(scale (m_i - M)). One warp per row, 16 bytes a lane.
+constexpr int kCombineWarps = 4;
+__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const TreeParams p) {
+  __shared__ float f_all[kCombineWarps][kMaxGrid];
+  __shared__ int at_all[kCombineWarps][kMaxGrid];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* f = f_all[warp];
+  int* at = at_all[warp];
   launch_dependents();
+  const long long row = (long long)blockIdx.x * kCombineWarps + warp;
+  const int r = (int)(row % p.rows), bh = (int)min(row / p.rows, (long long)p.B * p.Hkv - 1);
+  const int b = bh / p.Hkv, h = bh % p.Hkv;
   const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-  if (r % p.T >= s.draft) {
-    wait_for_predecessors();       // no kernel of the chain ends before the one it follows
-    return;
-  }
   const int wide = p.rows > BM ? 2 : 1;              // query tiles of a block
   const int block = r / (wide * BM), tile = r / BM % wide, tr = r % BM;
   int sum_all = 0, sum_before = 0;
@@ -593,10 +585,12 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
   const int nt = line_len(p, s);
   const long long a = per * __reduce_add_sync(0xffffffffu, sum_before) + ((long long)h * p.blocks + block) * nt;
   const int item = bh * p.blocks + block;
+  // no kernel of the chain ends before the one it follows
+  wait_for_predecessors();
+  if (row >= (long long)p.B * p.Hkv * p.rows || r % p.T >= s.draft) return;
   // the CTAs whose shares [total c / grid, total (c + 1) / grid) meet [a, a + nt)
   const int c0 = (int)(((a + 1) * p.grid + total - 1) / total) - 1;
   const int c1 = (int)(((a + nt) * p.grid + total - 1) / total) - 1;
-  wait_for_predecessors();
   if (c0 == c1) return;                              // one CTA had the whole item and wrote its rows
   int n = 0;
   float mx = -INFINITY;
@@ -609,8 +603,8 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
     const uint32_t v = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
     if (ml.x != -INFINITY) {
       const int q = n + __popc(v & ((1u << lane) - 1));
-      f[warp][q] = ml.x;
-      at[warp][q] = slot;
+      f[q] = ml.x;
+      at[q] = slot;
     }
     n += __popc(v);
     mx = fmaxf(mx, ml.x);
@@ -620,43 +614,30 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p) {
   __syncwarp();
   float l = 0.f;
   for (int q = lane; q < n; q += 32) {
-    const float k = fast_exp2((f[warp][q] - mx) * p.scale_log2);
-    l += k * p.part_ml[(long long)at[warp][q] * p.row_cap + tr].y;
-    f[warp][q] = k;
+    const float k = fast_exp2((f[q] - mx) * p.scale_log2);
+    l += k * p.part_ml[(long long)at[q] * p.row_cap + tr].y;
+    f[q] = k;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   __syncwarp();
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int q = warp; q < n; q += 4) {
-    const float k = f[warp][q];
+  for (int q = 0; q < n; ++q) {
+    const float k = f[q];
     const float4 v =
-        *reinterpret_cast<const float4*>(p.part_o + ((long long)at[warp][q] * p.row_cap + tr) * kHeadDim + 4 * lane);
+        *reinterpret_cast<const float4*>(p.part_o + ((long long)at[q] * p.row_cap + tr) * kHeadDim + 4 * lane);
     o.x += k * v.x;
     o.y += k * v.y;
     o.z += k * v.z;
     o.w += k * v.w;
   }
-  acc[warp][lane] = o;
-  __syncthreads();
-  const long long row = (long long)bh * p.rows + r;
-  if (warp == 0) {
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      const float4 v = acc[i][lane];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
-    }
-    const float g = l > 0.f ? 1.f / l : 0.f;
-    *reinterpret_cast<uint2*>(p.O + row * kHeadDim + 4 * lane) =
-        make_uint2(pack_bf16x2(o.x * g, o.y * g), pack_bf16x2(o.z * g, o.w * g));
-    if (lane == 0) {
-      if (p.lse) p.lse[row] = mx * p.scale + logf(l);
-      if (p.row_stat) p.row_stat[row] = make_float2(mx, 1.f / l);
-    }
+  const float g = l > 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(p.O + row * kHeadDim + 4 * lane) =
+      make_uint2(pack_bf16x2(o.x * g, o.y * g), pack_bf16x2(o.z * g, o.w * g));
+  if (lane == 0) {
+    if (p.lse) p.lse[row] = mx * p.scale + logf(l);
+    if (p.row_stat) p.row_stat[row] = make_float2(mx, 1.f / l);
   }
 }
 
@@ -703,11 +684,13 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   TreeMaps maps;
   if (!make_cache_map(enc, &maps.k, K, ks, B, Hkv, cap, BN) || !make_cache_map(enc, &maps.v, V, vs, B, Hkv, cap, BN))
     return DHSA_ERR_INVALID_ARG;
-  static bool done[2][64] = {{false}};
+  static bool done[3][64] = {{false}};
   int dev = 0, sms = 0;
   cudaError_t e = this_device(&dev, &sms);
-  auto* kernel = q.wide == 2 ? tree_attn_kernel<2> : tree_attn_kernel<1>;
-  if (e == cudaSuccess) e = allow_smem(kernel, (int)kSmemAlloc, dev, done[q.wide - 1]);
+  // rows beyond 64 need both halves of the lanes of each quarter
+  const int halves = q.rows > 64 ? 2 : 1;
+  auto* kernel = q.wide == 2 ? tree_attn_kernel<2, 2> : halves == 2 ? tree_attn_kernel<1, 2> : tree_attn_kernel<1, 1>;
+  if (e == cudaSuccess) e = allow_smem(kernel, (int)kSmemAlloc, dev, done[q.wide + halves - 2]);
   if (e != cudaSuccess) return cuda_status(e);
 
   TreeParams p;
@@ -746,10 +729,11 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = status;
-  kernel<<<p.grid, kThreads, kSmemAlloc, stream>>>(maps, p);
+  kernel<<<p.grid, block_threads(halves), kSmemAlloc, stream>>>(maps, p);
   int st = launch_status();
   if (st == DHSA_OK && !q.whole)
-    st = launch_after(tree_combine_kernel, dim3((unsigned)((long long)B * Hkv * q.rows)), dim3(128), 0, stream, p);
+    st = launch_after(tree_combine_kernel, dim3((unsigned)(((long long)B * Hkv * q.rows + kCombineWarps - 1) / kCombineWarps)),
+                      dim3(32 * kCombineWarps), 0, stream, p);
   if (st == DHSA_OK && weight_out && q.scores) {
     st = launch_tree_weight_scores(p, stream);
   } else if (st == DHSA_OK && weight_out) {

@@ -4,12 +4,17 @@
 //
 // The scores are computed again, transposed: S^T = K Q^T puts the slots on the
 // tensor core's M side, so that a thread owns a TMEM lane, one slot, and adds
-// its rows' p with no exchange between threads. K is read once more (256
+// its rows' p with no exchange between threads. The rows' statistics enter in
+// the tensor core too: two more steps of 16 columns, ones against -M and ones
+// against -log2(l) / scale (each as three bf16 parts), leave the exponent in
+// TMEM, so the epilogue reads nothing but its column. (Read from shared memory
+// per pair of rows instead, they took a quarter of the kernel's time.) K is read once more (256
 // bytes per slot); up to about 180 rows that read is the bound, above them
 // the exponentials (16 per cycle and SM).
 //
 // Warp 0 streams the K tiles, warp 1 issues the MMAs into two S^T buffers of
-// 256 columns, warps 4 to 7 take the even and warps 8 to 11 the odd tiles.
+// 256 columns; eight warps take the even and eight the odd tiles, four for each
+// half of the columns.
 // More than 256 rows walk the same keys again and add to weight_out.
 // Waits are bounded as in tree_attn.cu.
 #include <type_traits>
@@ -19,7 +24,7 @@
 namespace dhsa {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int BN = 128;                      // slots per key tile
 constexpr uint32_t kHalfBytes = BN * 128;    // 128 rows x 64 bf16, 128-byte swizzle
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
@@ -32,21 +37,40 @@ enum {
   W_QREADY = W_EMPTY + kStages,
   W_SFULL,                     // per buffer
   W_SEMPTY = W_SFULL + 2,
-  W_DONE = W_SEMPTY + 2,       // the eight warps have finished a walk
+  W_XSUM = W_SEMPTY + 2,       // [buffer][tile parity][lane quarter]: the upper columns' sums written
+  W_DONE = W_XSUM + 16,        // the sixteen warps have finished a walk
   W_FINAL,
   W_TEARDOWN,
   W_COUNT
 };
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_RING = 2 * kQHalfBytes;
-constexpr uint32_t OFF_STAT = OFF_RING + kStages * kTileBytes;     // float4 per pair of rows: -M0, -M1, 1/l0, 1/l1
-constexpr uint32_t OFF_SEE = OFF_STAT + kRowBlock / 2 * 16;        // per drafted token: those it sees
-constexpr uint32_t OFF_BAR = OFF_SEE + kMaxDrafts * 8;
+constexpr uint32_t OFF_ONES = OFF_RING + kStages * kTileBytes;     // the statistics' operands, 16 columns, not swizzled:
+constexpr uint32_t OFF_BIAS = OFF_ONES + BN * 32;                  //   ones for each slot; -M and -log l for each row
+constexpr uint32_t OFF_SEE = OFF_BIAS + 2 * kRowBlock * 32;        // per drafted token: those it sees
+constexpr uint32_t OFF_XSUM = OFF_SEE + kMaxDrafts * 8;            // [buffer][tile parity][slot]
+constexpr uint32_t OFF_BAR = OFF_XSUM + 4 * BN * 4;
 constexpr uint32_t OFF_LINE = OFF_BAR + 8 * ((W_COUNT + 1) & ~1);
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
+
+// byte offset of element (row, k) of a 16-column bf16 operand without swizzle
+__device__ __forceinline__ uint32_t noswz_off(int row, int k) {
+  return (uint32_t)((row >> 3) * 256 + (k >> 3) * 128 + (row & 7) * 16 + (k & 7) * 2);
+}
+// an fp32 value as the sum of three bf16 values, 8 significant bits each
+__device__ __forceinline__ void write_parts(unsigned char* at, float x) {
+  const __nv_bfloat16 hi = __float2bfloat16(x);
+  const float r1 = x - __bfloat162float(hi);
+  const __nv_bfloat16 mid = __float2bfloat16(r1);
+  const __nv_bfloat16 lo = __float2bfloat16(r1 - __bfloat162float(mid));
+  __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(at);
+  d[0] = hi;
+  d[1] = mid;
+  d[2] = lo;
+}
 
 __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                   const TreeParams p) {
@@ -56,8 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   Line* line = reinterpret_cast<Line*>(smem + OFF_LINE);
-  float4* stat = reinterpret_cast<float4*>(smem + OFF_STAT);
   uint64_t* see = reinterpret_cast<uint64_t*>(smem + OFF_SEE);
+  float* xsum = reinterpret_cast<float*>(smem + OFF_XSUM);
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -68,12 +92,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         mbar_init(bar(W_FULL + s), 1);
         mbar_init(bar(W_EMPTY + s), 1);
       }
-      mbar_init(bar(W_QREADY), 8);
+      mbar_init(bar(W_QREADY), 16);
       for (int s = 0; s < 2; ++s) {
         mbar_init(bar(W_SFULL + s), 1);
-        mbar_init(bar(W_SEMPTY + s), 4);
+        mbar_init(bar(W_SEMPTY + s), 8);
       }
-      mbar_init(bar(W_DONE), 8);
+      for (int s = 0; s < 16; ++s) mbar_init(bar(W_XSUM + s), 1);
+      mbar_init(bar(W_DONE), 16);
       mbar_init(bar(W_FINAL), 1);
       mbar_init(bar(W_TEARDOWN), kThreads / 32 - 1);
       fence_mbar_init();
@@ -86,6 +111,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
     const Line L = find_share(p, blockIdx.x, lane);
     if (lane == 0) *line = L;
   }
+  for (uint32_t o = threadIdx.x * 16; o < OFF_SEE - OFF_ONES; o += kThreads * 16)
+    *reinterpret_cast<uint4*>(smem + OFF_ONES + o) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  for (int i = threadIdx.x; i < 3 * BN; i += kThreads)
+    *reinterpret_cast<__nv_bfloat16*>(smem + OFF_ONES + noswz_off(i / 3, i % 3)) = __float2bfloat16(1.f);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -142,6 +173,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
               mma_ss(tmem + s * 256, smem_desc_sw128(ka + (k >> 2) * kHalfBytes + c, 16, 1024),
                      smem_desc_sw128(sbase + OFF_Q + (k >> 2) * kQHalfBytes + c, 16, 1024), idesc, k > 0 ? 1u : 0u);
             }
+            // S - M first, as an exact difference of like numbers, then - log l
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_ss(tmem + s * 256, smem_desc_noswz(sbase + OFF_ONES, 128, 256),
+                     smem_desc_noswz(sbase + OFF_BIAS + k * kRowBlock * 32, 128, 256), idesc, 1u);
             mma_commit(bar(W_SFULL + s));
             mma_commit(bar(W_EMPTY + st));
           }
@@ -151,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
       mbar_wait(bar(W_FINAL), 0, kWaitLimitNs);
     }
   } else if (warp >= 4) {
-    const int buf = (warp - 4) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    // per S^T buffer two groups of four warps, one for each half of the columns
+    const int buf = ((warp - 4) >> 2) & 1, upper = (warp - 4) >> 3, quarter = warp & 3, key = quarter * 32 + lane;
     const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256;
     const float c = p.scale_log2;
     const uint64_t c2 = pk2(c, c);
@@ -170,48 +207,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         see[lane + 32] = sv.m1;
       }
       for (int rb = 0; ok && rb < walks; ++rb) {
-        // the Q operand and the row statistics: 32 rows per warp. Rows past
+        // the Q operand and the row statistics: 16 rows per warp. Rows past
         // the end and of missing tokens are zeros with weight 0.
         const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock), n_pad = (n_rows + 31) & ~31;
         const int ch = lane & 15;
+        uint4 v[8];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {       // eight loads in flight
-          uint4 v[8];
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int at = (warp - 4) * 32 + half * 16 + it * 2 + (lane >> 4), r = rb * kRowBlock + at;
-            v[it] = make_uint4(0, 0, 0, 0);
-            if (at < n_rows && r % p.T < w.draft)
-              v[it] = *reinterpret_cast<const uint4*>(p.Q + (row_base + r) * kHeadDim + ch * 8);
-          }
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int at = (warp - 4) * 32 + half * 16 + it * 2 + (lane >> 4);
-            if (at < n_pad)
-              *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * kQHalfBytes + at * 128 +
-                                        (((ch & 7) ^ (at & 7)) << 4)) = v[it];
-          }
+        for (int it = 0; it < 8; ++it) {
+          const int at = (warp - 4) * 16 + it * 2 + (lane >> 4), r = rb * kRowBlock + at;
+          v[it] = make_uint4(0, 0, 0, 0);
+          if (at < n_rows && r % p.T < w.draft)
+            v[it] = *reinterpret_cast<const uint4*>(p.Q + (row_base + r) * kHeadDim + ch * 8);
         }
-        {
-          const int at = (warp - 4) * 32 + lane, r = rb * kRowBlock + at;
-          const int t = r % p.T;
-          float2 st = make_float2(0.f, 0.f);
-          if (at < n_rows && t < w.draft) st = p.row_stat[row_base + r];
-          float* f = reinterpret_cast<float*>(stat + at / 2);
-          f[at & 1] = -st.x;
-          f[2 + (at & 1)] = st.y;
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int at = (warp - 4) * 16 + it * 2 + (lane >> 4);
+          if (at < n_pad)
+            *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * kQHalfBytes + at * 128 +
+                                      (((ch & 7) ^ (at & 7)) << 4)) = v[it];
+        }
+        if (lane < 16) {
+          const int at = (warp - 4) * 16 + lane, r = rb * kRowBlock + at;
+          float minus_m = -INFINITY, minus_log = 0.f;
+          if (at < n_rows && r % p.T < w.draft) {
+            const float2 st = p.row_stat[row_base + r];
+            minus_m = -st.x;
+            minus_log = __log2f(st.y) / c;
+          }
+          if (at < n_pad) {
+            unsigned char* m_at = smem + OFF_BIAS + noswz_off(at, 0);
+            if (minus_m == -INFINITY) {      // no inf - inf in the lower parts
+              *reinterpret_cast<uint2*>(m_at) = make_uint2(0xFF80u, 0u);
+            } else {
+              write_parts(m_at, minus_m);
+            }
+            write_parts(m_at + kRowBlock * 32, minus_log);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(W_QREADY));
-        // the statistics are read by all eight warps
-        if (!(ok = wait(bar(W_QREADY), n_done & 1))) break;
 
         for (int i = buf; i < w.n; i += 2) {
           const int slot = (w.t0 + i) * BN + key;
           const bool live = slot < slots;
           float old = 0.f;
-          if (live) old = rb > 0 ? w_out[slot] : slot < w.len ? w_in[slot] : 0.f;
+          if (live && !upper) old = rb > 0 ? w_out[slot] : slot < w.len ? w_in[slot] : 0.f;
           if (!(ok = wait(bar(W_SFULL + buf), n_s & 1))) break;
           ++n_s;
           tc_fence_after();
@@ -223,16 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
             seen = 0;
             for (int t = 0; t < w.draft; ++t) seen |= ((see[t] >> (d & 63)) & 1) << t;
           }
-          int t = rb * kRowBlock % p.T;
+          const int n_half = n_pad / 2, col0 = upper * n_half;      // this warp's columns
+          int t = (rb * kRowBlock + col0) % p.T;
           uint64_t acc[2] = {0ull, 0ull};
-          // 32 rows: their p, weighed and added in pairs
-          auto add = [&](auto with_mask, const uint32_t (&s)[32], int r0) {
+          // 16 rows: their p, added in pairs
+          auto add = [&](auto with_mask, const uint32_t (&s)[16]) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float4 st = stat[(r0 + e) / 2];
-              const uint64_t x = mul2(add2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pk2(st.x, st.y)), c2);
+            for (int e = 0; e < 16; e += 2) {
               float x0, x1;
-              unpk2(x, x0, x1);
+              unpk2(mul2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2), x0, x1);
               x0 = fast_exp2(x0);
               x1 = fast_exp2(x1);
               if (with_mask.value) {
@@ -241,22 +281,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
                 x1 = (seen >> t) & 1 ? x1 : 0.f;
                 t = t + 1 == p.T ? 0 : t + 1;
               }
-              acc[(e >> 1) & 1] = fma2(pk2(x0, x1), pk2(st.z, st.w), acc[(e >> 1) & 1]);
+              acc[(e >> 1) & 1] = add2(acc[(e >> 1) & 1], pk2(x0, x1));
             }
           };
-          // the next 32 columns are on their way while these are added
+          // the next 16 columns are on their way while these are added
           auto add_all = [&](auto with_mask) {
-            uint32_t s0[32], s1[32];
-            tmem_ld32(tS, s0);
+            uint32_t s0[16], s1[16];
+            tmem_ld16(tS + col0, s0);
             tmem_wait_ld();
 #pragma unroll 1
-            for (int r0 = 0; r0 < n_pad; r0 += 64) {
-              if (r0 + 32 < n_pad) tmem_ld32(tS + r0 + 32, s1);
-              add(with_mask, s0, r0);
-              if (r0 + 32 >= n_pad) break;
+            for (int r0 = 0; r0 < n_half; r0 += 32) {
+              if (r0 + 16 < n_half) tmem_ld16(tS + col0 + r0 + 16, s1);
+              add(with_mask, s0);
+              if (r0 + 16 >= n_half) break;
               tmem_wait_ld();
-              if (r0 + 64 < n_pad) tmem_ld32(tS + r0 + 64, s0);
-              add(with_mask, s1, r0 + 32);
+              if (r0 + 32 < n_half) tmem_ld16(tS + col0 + r0 + 32, s0);
+              add(with_mask, s1);
               tmem_wait_ld();
             }
           };
@@ -267,7 +307,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
           if (lane == 0) mbar_arrive(bar(W_SEMPTY + buf));
           float a0, a1;
           unpk2(add2(acc[0], acc[1]), a0, a1);
-          if (live) w_out[slot] = old + (a0 + a1);
+          // the lower columns' warp adds the upper columns' sums and writes
+          const int x = buf * 2 + (int)((n_s - 1) & 1);
+          if (upper) {
+            xsum[x * BN + key] = a0 + a1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(W_XSUM + x * 4 + quarter));
+          } else {
+            if (!(ok = wait(bar(W_XSUM + x * 4 + quarter), ((n_s - 1) >> 1) & 1))) break;
+            if (live) w_out[slot] = old + (a0 + a1 + xsum[x * BN + key]);
+          }
         }
         if (!ok) break;
         // Q and the statistics may change once every warp is done with them
