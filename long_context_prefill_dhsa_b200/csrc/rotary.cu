@@ -20,7 +20,7 @@
 namespace dhsa {
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 constexpr int kUnits = kHeadDim / 16;   // threads per row
 constexpr int kHeadsInFlight = 4;       // rows a thread has loaded at a time
 
@@ -69,7 +69,8 @@ __device__ __forceinline__ void turn(uint4& x, uint4& y, const float (&c)[8], co
   y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
 }
 
-template <bool INTERLEAVED>
+// STREAM: the outputs do not fit in L2
+template <bool INTERLEAVED, bool STREAM>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
   const long long idx = (long long)blockIdx.x * kRotThreads + threadIdx.x;
   const int u = (int)(idx % kUnits);
@@ -147,8 +148,14 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     for (int k = 0; k < kHeadsInFlight; ++k) {
       if (!dst[k]) continue;
       if (rotated && r0 + k < p.Hq + p.Hkv) turn<INTERLEAVED>(x[k], y[k], c, s);
-      *reinterpret_cast<uint4*>(dst[k] + e0) = x[k];
-      *reinterpret_cast<uint4*>(dst[k] + e1) = y[k];
+      uint4 *d0 = reinterpret_cast<uint4*>(dst[k] + e0), *d1 = reinterpret_cast<uint4*>(dst[k] + e1);
+      if (STREAM) {
+        __stcs(d0, x[k]);
+        __stcs(d1, y[k]);
+      } else {
+        *d0 = x[k];
+        *d1 = y[k];
+      }
     }
   }
 }
@@ -190,14 +197,22 @@ int launch_rotary(const void* Q, const RowStrides& qs, const void* K, const RowS
   p.status = status;
   const int rows = p.rows = p.Hq + (V ? 2 : K ? 1 : 0) * Hkv;
   const long long blocks = ((long long)B * T * kUnits + kRotThreads - 1) / kRotThreads;
-  // few tokens: spread the heads over blocks until about 8 blocks per SM exist
+  // Few tokens: spread the heads over blocks until four blocks per SM exist.
+  // More groups repeat the cosines and sines: 18 rows of 16K tokens take 29.7
+  // us in 1024 blocks and 35.9 us in four times as many; the 40 rows of 32K
+  // tokens are the same either way (113 us).
   int groups = 1;
-  while (blocks * groups < 8 * 148 && groups < rows) groups *= 2;
+  while (blocks * groups < 4 * 148 && groups < rows) groups *= 2;
+  // Outputs beyond L2 (126 MB) are written past it: 108.5 against 112.9 us at
+  // 335 MB; outputs that fit stay there for the next kernel (75 MB: 29.7
+  // against 32.6 us even for this one).
+  const bool past_l2 = (long long)B * T * rows * kHeadDim * 2 > 96ll << 20;
   p.heads_per_group = ceil_div(rows, groups);
   groups = ceil_div(rows, p.heads_per_group);
   const dim3 grid((unsigned)blocks, (unsigned)groups);
-  if (interleaved) rotary_kernel<true><<<grid, kRotThreads, 0, stream>>>(p);
-  else rotary_kernel<false><<<grid, kRotThreads, 0, stream>>>(p);
+  auto* kernel = interleaved ? (past_l2 ? rotary_kernel<true, true> : rotary_kernel<true, false>)
+                             : (past_l2 ? rotary_kernel<false, true> : rotary_kernel<false, false>);
+  kernel<<<grid, kRotThreads, 0, stream>>>(p);
   return launch_status();
 }
 
