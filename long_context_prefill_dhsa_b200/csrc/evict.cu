@@ -34,7 +34,7 @@ constexpr int kBins = 256;
 constexpr int kParts = kEvThreads / kBins;
 constexpr int kRounds = 4;
 constexpr int kMaxCluster = 16;           // above 8 the launch asks for the non-portable size
-constexpr int kBatch = 8;                 // slots whose weight and position a thread loads at a time
+constexpr int kBatch = 4;                 // slots whose weight and position a thread loads at a time
 constexpr int kKeysPerBlock = 48 * 1024;  // keys held in shared memory; later ones are derived again
 constexpr int kSlotsPerBlock = 8192;      // slots a block of a cluster is given before another one joins
 
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
       }
     }
     uint32_t left = (uint32_t)m;
-#pragma unroll
+#pragma unroll 1
     for (int r = 0; r < kRounds; ++r) {
       const int shift = 24 - 8 * r;
       if (r > 0) {
@@ -165,7 +165,11 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
       {
         uint32_t v = 0;
         const int bin = tid & 255;
-        for (int c = tid >> 8; c < C; c += kParts) v += cluster.map_shared_rank(&sh.hist[r][0], c)[bin];
+#pragma unroll
+        for (int i = 0; i < kMaxCluster / kParts; ++i) {       // all in flight at once
+          const int c = (tid >> 8) + i * kParts;
+          if (c < C) v += cluster.map_shared_rank(&sh.hist[r][0], c)[bin];
+        }
         sh.part[tid >> 8][bin] = v;
       }
       __syncthreads();

@@ -15,6 +15,7 @@ struct TreeParams {
   float2* row_stat;         // per row: largest raw score and 1 / denominator, for the weight pass (null without)
   float* scores;            // [B * Hkv][rows][score_cap] raw scores for the weight pass, or null
   float* part_o;            // [piece][query tile][row_cap][128]
+  int2* span;               // per item: the first and the last CTA that had a part of it
   float2* part_ml;          // [piece][query tile][row_cap]: reference score and sum
   const float* weight;
   float* weight_out;
@@ -23,7 +24,6 @@ struct TreeParams {
   int blocks;               // query blocks of a kv head that walk the keys
   int row_cap;              // rows of a query tile's partial
   int score_cap;            // cap rounded up to whole key tiles
-  int tile;                 // slots of a key tile
   int grid;                 // CTAs that share the key tiles
   bool whole;               // items are not split: the line counts items instead of key tiles
   bool keep_k;              // K is read again after this kernel
@@ -41,11 +41,12 @@ constexpr int kMaxGroup = 64;    // query heads of one kv head
 constexpr int kMaxScoreRows = 32;   // rows of a head up to which the attention keeps its scores for the weight pass
 constexpr int kMaxGrid = 160;    // CTAs (one per SM) the workspace is sized for
 
+constexpr int kTileSlots = 128;  // slots of a key tile
 constexpr uint32_t kTmemCols = 512;
 
 // key tiles of each item of a sequence, and the item's length on the line
 __device__ __forceinline__ int key_tiles(const TreeParams& p, const SeqLen& s) {
-  return s.draft > 0 || p.every ? (s.len + s.draft + p.tile - 1) / p.tile : 0;
+  return s.draft > 0 || p.every ? (s.len + s.draft + kTileSlots - 1) / kTileSlots : 0;
 }
 __device__ __forceinline__ int line_len(const TreeParams& p, const SeqLen& s) {
   const int n = key_tiles(p, s);
@@ -55,41 +56,90 @@ __device__ __forceinline__ int line_len(const TreeParams& p, int b) {
   return line_len(p, seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap));
 }
 
-// The line of key tiles: sequence b's items start at `base`.
+// The line of key tiles, and how it is cut: sequence b's items start at
+// `base`, and the CTA has [start, end).
+//
+// With fewer items than CTAs each item gets a whole number of CTAs in
+// proportion to its tiles (`each` of them in sequence b, the first being CTA
+// `first`), so that no CTA has parts of two: such a CTA would drain one item
+// and fill its pipeline again for the next, about as long as five tiles. With
+// more items the line is cut into equal shares.
+// (At most 2^31 cached slots and 32 query blocks: the line is shorter than 2^30.)
 struct Line {
-  long long total, start, end, base;
-  int b;
+  int start, end, base, b;
 };
 
-// by one warp: the whole line's length, and the share of CTA c with the
-// sequence it starts in
+// start of share c of a line cut into `grid` equal shares: total c / grid
+__device__ __forceinline__ int share_start(int total, int grid, int c) {
+  return total / grid * c + total % grid * c / grid;
+}
+// CTAs that each item of a sequence with n tiles gets when the line is cut by items
+__device__ __forceinline__ int item_ctas(const TreeParams& p, int n, int total) {
+  return n ? max(1, min(n, (int)((unsigned)p.grid * (unsigned)n / (unsigned)total))) : 0;
+}
+
+// by one warp: the share of CTA c, with the sequence it starts in and that
+// sequence's place. A line cut into equal shares is at least as long as there
+// are CTAs, so no share of it is empty: shorter ones, and those with fewer
+// items than CTAs, are cut by items (unless small items would take more CTAs
+// than there are).
 __device__ __forceinline__ Line find_share(const TreeParams& p, int c, int lane) {
-  Line L;
-  const long long per = (long long)p.Hkv * p.blocks;
-  int sum = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) sum += b0 + lane < p.B ? line_len(p, b0 + lane) : 0;
-  L.total = per * __reduce_add_sync(0xffffffffu, sum);
-  L.start = L.total * c / p.grid;
-  L.end = L.total * (c + 1) / p.grid;
-  L.base = 0;
-  L.b = 0;
-  long long run = 0;
-  for (int b0 = 0; b0 < p.B && run <= L.start; b0 += 32) {
-    const int n = b0 + lane < p.B ? line_len(p, b0 + lane) : 0;
-    int inc = n;
-#pragma unroll
+  const int per = p.Hkv * p.blocks;
+  const int n0 = lane < p.B ? line_len(p, lane) : 0;
+  auto len_of = [&](int b0) { return b0 == 0 ? n0 : b0 + lane < p.B ? line_len(p, b0 + lane) : 0; };
+  int sum = 0, some = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int n = len_of(b0);
+    sum += n;
+    some += n > 0;
+  }
+  const int total = per * __reduce_add_sync(0xffffffffu, sum);
+  some = __reduce_add_sync(0xffffffffu, some);
+  Line L{0, 0, 0, 0};
+  if (total == 0) return L;
+  bool by_item = (long long)some * per <= p.grid && !p.whole;
+  if (by_item) {
+    int ctas = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32) ctas += item_ctas(p, len_of(b0), total);
+    by_item = per * __reduce_add_sync(0xffffffffu, ctas) <= p.grid;
+  }
+  if (!by_item) {
+    L.start = share_start(total, p.grid, c);
+    L.end = share_start(total, p.grid, c + 1);
+  }
+  // the sequence that holds the share's start, or, by items, CTA c
+  const int want = by_item ? c : L.start;
+  int run = 0, run_base = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B && run <= want; b0 += 32) {
+    const int n = len_of(b0), k = by_item ? item_ctas(p, n, total) : n;
+    int inc = k, inc_n = n;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const int v = __shfl_up_sync(0xffffffffu, inc, o), vn = __shfl_up_sync(0xffffffffu, inc_n, o);
+      if (lane >= o) {
+        inc += v;
+        inc_n += vn;
+      }
     }
-    const long long from = run + (inc - n) * per, to = run + inc * per;
-    const uint32_t hit = __ballot_sync(0xffffffffu, from <= L.start && L.start < to);
+    const int from = run + (inc - k) * per, to = run + inc * per;
+    const uint32_t hit = __ballot_sync(0xffffffffu, from <= want && want < to);
     if (hit) {
       const int src = __ffs(hit) - 1;
       L.b = b0 + src;
-      L.base = __shfl_sync(0xffffffffu, from, src);
+      L.base = run_base + __shfl_sync(0xffffffffu, inc_n - n, src) * per;
+      if (by_item) {
+        const int rel = c - __shfl_sync(0xffffffffu, from, src), each = __shfl_sync(0xffffffffu, k, src);
+        const int nt = __shfl_sync(0xffffffffu, n, src), item = rel / each, part = rel % each;
+        L.start = L.base + item * nt + share_start(nt, each, part);
+        L.end = L.base + item * nt + share_start(nt, each, part + 1);
+      }
+      break;
     }
     run += __shfl_sync(0xffffffffu, inc, 31) * per;
+    run_base += __shfl_sync(0xffffffffu, inc_n, 31) * per;
   }
   return L;
 }
@@ -97,18 +147,19 @@ __device__ __forceinline__ Line find_share(const TreeParams& p, int c, int lane)
 struct Piece {
   int b, h, block;
   int t0, n;            // key tiles t0 .. t0 + n - 1 of the item
-  bool complete;        // they are all of its tiles
+  bool first, complete; // they begin the item; they are all of its tiles
+  bool last;            // they end it
   int len, draft;
   int item;
 };
 
 // walks a CTA's share; every role does so on its own
 struct Pieces {
-  long long pos, end, base;
+  int pos, end, base;
   int b;
   __device__ __forceinline__ bool next(const TreeParams& p, Piece* o) {
     if (pos >= end) return false;
-    const long long per = (long long)p.Hkv * p.blocks;
+    const int per = p.Hkv * p.blocks;
     SeqLen s;
     int nt;
     for (;; ++b) {      // pos < end: a sequence with tiles follows
@@ -117,14 +168,15 @@ struct Pieces {
       if (pos < base + nt * per) break;
       base += nt * per;
     }
-    const unsigned rel = (unsigned)(pos - base);    // below 2^31 tiles of one sequence
+    const unsigned rel = (unsigned)(pos - base);
     const unsigned in_b = rel / (unsigned)nt;
     o->b = b;
     o->h = in_b / p.blocks;
     o->block = in_b % p.blocks;
     o->t0 = rel % (unsigned)nt;
-    const long long left = end - pos;
-    const int n = (int)min((long long)(nt - o->t0), left);
+    const int n = min(nt - o->t0, end - pos);
+    o->first = o->t0 == 0;
+    o->last = o->t0 + n == nt;
     o->complete = n == nt;
     o->n = p.whole ? key_tiles(p, s) : n;
     o->len = s.len;

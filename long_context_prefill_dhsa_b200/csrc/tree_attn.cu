@@ -12,9 +12,9 @@
 // sm_100a design
 // --------------
 // * Work: the 128-slot key tiles of all (sequence, kv head, query block) items
-//   are one line, cut into equal shares, one per CTA of a persistent grid; a
-//   share covers the end of one item, some whole ones and the start of
-//   another. Lengths are read on the device, so ragged batches balance
+//   are one line, cut into shares, one per CTA of a persistent grid (tree.cuh):
+//   parts of one item each while there are CTAs for every item, equal shares
+//   of the line beyond that. Lengths are read on the device, so ragged batches balance
 //   without host help. A CTA that has all of an item writes its rows; the
 //   others leave an unnormalised O with its reference score and sum for each
 //   piece, and a second kernel joins an item's pieces.
@@ -41,7 +41,6 @@
 
 namespace dhsa {
 
-int tree_weight_tile();
 int launch_tree_weight_scores(const TreeParams& p, cudaStream_t stream);
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream);
 
@@ -89,6 +88,7 @@ constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;   // slack for aligning the base
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 static_assert(sizeof(Line) % 8 == 0, "alignment");
+static_assert(BN == kTileSlots, "the line is cut into these tiles");
 
 constexpr int W_PRODUCER = 0, W_MMA = 1, W_SOFTMAX0 = 4;
 
@@ -451,6 +451,10 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
       }
       if (!ok) break;
       g += 2 * w.n;
+      if (warp == W_SOFTMAX0 && lane == 0 && !p.whole) {
+        if (w.first) p.span[w.item].x = blockIdx.x;
+        if (w.last) p.span[w.item].y = blockIdx.x;
+      }
       // ---- the piece's result
       if (!(ok = wait(bar(B_OFINAL), n_piece & 1))) break;
       tc_fence_after();
@@ -575,28 +579,18 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
   const int wide = p.rows > BM ? 2 : 1;              // query tiles of a block
   const int block = r / (wide * BM), tile = r / BM % wide, tr = r % BM;
-  int sum_all = 0, sum_before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int n = b0 + lane < p.B ? line_len(p, b0 + lane) : 0;
-    sum_all += n;
-    sum_before += b0 + lane < b ? n : 0;
-  }
-  const long long per = (long long)p.Hkv * p.blocks, total = per * __reduce_add_sync(0xffffffffu, sum_all);
-  const int nt = line_len(p, s);
-  const long long a = per * __reduce_add_sync(0xffffffffu, sum_before) + ((long long)h * p.blocks + block) * nt;
   const int item = bh * p.blocks + block;
   // no kernel of the chain ends before the one it follows
   wait_for_predecessors();
   if (row >= (long long)p.B * p.Hkv * p.rows || r % p.T >= s.draft) return;
-  // the CTAs whose shares [total c / grid, total (c + 1) / grid) meet [a, a + nt)
-  const int c0 = (int)(((a + 1) * p.grid + total - 1) / total) - 1;
-  const int c1 = (int)(((a + nt) * p.grid + total - 1) / total) - 1;
+  const int2 span = p.span[item];
+  const int c0 = span.x, c1 = span.y;
   if (c0 == c1) return;                              // one CTA had the whole item and wrote its rows
   int n = 0;
   float mx = -INFINITY;
   for (int x0 = c0; x0 <= c1; x0 += 32) {
     const int c = x0 + lane;
-    const bool has = c <= c1 && total * c / p.grid < total * (c + 1) / p.grid;
+    const bool has = c <= c1;
     const int slot = (c + item) * wide + tile;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (has) ml = p.part_ml[(long long)slot * p.row_cap + tr];
@@ -644,7 +638,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
 struct Plan {
   int rows, wide, blocks, row_cap, score_cap;
   bool whole, scores;
-  size_t o_bytes, ml_bytes, stat_bytes, score_bytes;
+  size_t o_bytes, ml_bytes, span_bytes, stat_bytes, score_bytes;
 };
 Plan make_plan(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
   Plan q;
@@ -659,6 +653,7 @@ Plan make_plan(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
   auto round = [](size_t n) { return (n + 255) / 256 * 256; };
   q.o_bytes = round(pieces * q.wide * q.row_cap * kHeadDim * sizeof(float));
   q.ml_bytes = round(pieces * q.wide * q.row_cap * sizeof(float2));
+  q.span_bytes = q.whole ? 0 : round(sizeof(int2) * (size_t)B * Hkv * q.blocks);
   q.stat_bytes = want_weight ? round(sizeof(float2) * (size_t)B * Hq * T) : 0;
   q.score_bytes = q.scores ? sizeof(float) * (size_t)B * Hkv * q.rows * q.score_cap : 0;
   return q;
@@ -671,7 +666,7 @@ int tree_max_group() { return kMaxGroup; }
 
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
   const Plan q = make_plan(B, Hq, Hkv, T, cap, want_weight);
-  return 256 + q.o_bytes + q.ml_bytes + q.stat_bytes + q.score_bytes;
+  return 256 + q.o_bytes + q.ml_bytes + q.span_bytes + q.stat_bytes + q.score_bytes;
 }
 
 int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const void* V, const RowStrides& vs, int B,
@@ -703,7 +698,8 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   char* at = static_cast<char*>(ws);
   p.part_o = reinterpret_cast<float*>(at);
   p.part_ml = reinterpret_cast<float2*>(at += q.o_bytes);
-  p.row_stat = reinterpret_cast<float2*>(at += q.ml_bytes);
+  p.span = reinterpret_cast<int2*>(at += q.ml_bytes);
+  p.row_stat = reinterpret_cast<float2*>(at += q.span_bytes);
   p.scores = reinterpret_cast<float*>(at += q.stat_bytes);
   if (!weight_out) p.row_stat = nullptr;
   if (!q.scores) p.scores = nullptr;
@@ -719,7 +715,6 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.blocks = q.blocks;
   p.row_cap = q.row_cap;
   p.every = false;
-  p.tile = BN;
   p.score_cap = q.score_cap;
   p.whole = q.whole;
   p.keep_k = weight_out && !q.scores;
@@ -740,12 +735,11 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
     p.whole = false;
     p.every = true;                   // weights without new tokens are passed on
     p.blocks = 1;                     // one walk over the keys for all rows of a head
-    p.tile = tree_weight_tile();
     p.grid = sms < kMaxGrid ? sms : kMaxGrid;
-    const long long tiles = (long long)B * Hkv * ceil_div(cap, p.tile);
+    const long long tiles = (long long)B * Hkv * ceil_div(cap, kTileSlots);
     if (tiles < p.grid) p.grid = (int)tiles;
     CUtensorMap kmap;
-    if (!make_cache_map(enc, &kmap, K, ks, B, Hkv, cap, p.tile)) return DHSA_ERR_INVALID_ARG;
+    if (!make_cache_map(enc, &kmap, K, ks, B, Hkv, cap, kTileSlots)) return DHSA_ERR_INVALID_ARG;
     st = launch_tree_weight(kmap, p, stream);
   }
   return st;

@@ -55,6 +55,7 @@ constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
+static_assert(BN == kTileSlots, "the line is cut into these tiles");
 
 // byte offset of element (row, k) of a 16-column bf16 operand without swizzle
 __device__ __forceinline__ uint32_t noswz_off(int row, int k) {
@@ -383,8 +384,6 @@ __global__ void __launch_bounds__(kSlotThreads) tree_weight_scores_kernel(const 
 }
 
 }  // namespace
-
-int tree_weight_tile() { return BN; }
 
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream) {
   static bool done[64] = {false};
