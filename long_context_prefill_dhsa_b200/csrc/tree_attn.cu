@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     fence_mbar_init();
   }
   __syncthreads();
-  launch_dependents();
   // The producer needs nothing but the barriers and its share: it starts the
   // copies while the others allocate TMEM and look up theirs.
   Line share;
@@ -564,25 +563,25 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
 }
 
 // Joins the pieces of a row that several CTAs share: O = sum_i f_i O_i /
-// sum_i f_i l_i, f_i = exp(scale (m_i - M)). One warp per row, 16 bytes a lane.
-constexpr int kCombineWarps = 4;
-__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const TreeParams p) {
-  __shared__ float f_all[kCombineWarps][kMaxGrid];
-  __shared__ int at_all[kCombineWarps][kMaxGrid];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* f = f_all[warp];
-  int* at = at_all[warp];
+// sum_i f_i l_i, f_i = exp(scale (m_i - M)). One block of one warp per row, 16
+// bytes a lane. (Blocks of four warps took 1 to 3 us more, and so did letting
+// them start while the attention runs: they then crowd on the SMs that are
+// free first.)
+__global__ void __launch_bounds__(32) tree_combine_kernel(const TreeParams p) {
+  __shared__ float f[kMaxGrid];
+  __shared__ int at[kMaxGrid];
+  const int lane = threadIdx.x;
   launch_dependents();
-  const long long row = (long long)blockIdx.x * kCombineWarps + warp;
-  const int r = (int)(row % p.rows), bh = (int)min(row / p.rows, (long long)p.B * p.Hkv - 1);
-  const int b = bh / p.Hkv, h = bh % p.Hkv;
+  const long long row = blockIdx.x;
+  const int r = (int)(row % p.rows), bh = (int)(row / p.rows);
+  const int b = bh / p.Hkv;
   const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
   const int wide = p.rows > BM ? 2 : 1;              // query tiles of a block
   const int block = r / (wide * BM), tile = r / BM % wide, tr = r % BM;
   const int item = bh * p.blocks + block;
   // no kernel of the chain ends before the one it follows
   wait_for_predecessors();
-  if (row >= (long long)p.B * p.Hkv * p.rows || r % p.T >= s.draft) return;
+  if (r % p.T >= s.draft) return;
   const int2 span = p.span[item];
   const int c0 = span.x, c1 = span.y;
   if (c0 == c1) return;                              // one CTA had the whole item and wrote its rows
@@ -727,8 +726,7 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   kernel<<<p.grid, block_threads(halves), kSmemAlloc, stream>>>(maps, p);
   int st = launch_status();
   if (st == DHSA_OK && !q.whole)
-    st = launch_after(tree_combine_kernel, dim3((unsigned)(((long long)B * Hkv * q.rows + kCombineWarps - 1) / kCombineWarps)),
-                      dim3(32 * kCombineWarps), 0, stream, p);
+    st = launch_after(tree_combine_kernel, dim3((unsigned)((long long)B * Hkv * q.rows)), dim3(32), 0, stream, p);
   if (st == DHSA_OK && weight_out && q.scores) {
     st = launch_tree_weight_scores(p, stream);
   } else if (st == DHSA_OK && weight_out) {
