@@ -35,9 +35,9 @@ enum {
   W_FULL = 0,
   W_EMPTY = W_FULL + kStages,
   W_QREADY = W_EMPTY + kStages,
-  W_SFULL,                     // per buffer
-  W_SEMPTY = W_SFULL + 2,
-  W_XSUM = W_SEMPTY + 2,       // [buffer][tile parity][lane quarter]: the upper columns' sums written
+  W_SFULL,                     // [buffer][half of the columns]
+  W_SEMPTY = W_SFULL + 4,
+  W_XSUM = W_SEMPTY + 4,       // [buffer][tile parity][lane quarter]: the upper columns' sums written
   W_DONE = W_XSUM + 16,        // the sixteen warps have finished a walk
   W_FINAL,
   W_TEARDOWN,
@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         mbar_init(bar(W_EMPTY + s), 1);
       }
       mbar_init(bar(W_QREADY), 16);
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 4; ++s) {
         mbar_init(bar(W_SFULL + s), 1);
-        mbar_init(bar(W_SEMPTY + s), 8);
+        mbar_init(bar(W_SEMPTY + s), 4);
       }
       for (int s = 0; s < 16; ++s) mbar_init(bar(W_XSUM + s), 1);
       mbar_init(bar(W_DONE), 16);
@@ -159,27 +159,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         for (int rb = 0; ok && rb < walks; ++rb) {
           if (!(ok = wait(bar(W_QREADY), n_q++ & 1))) break;
           const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock);
-          const uint32_t idesc = idesc_bf16_f32(BN, (n_rows + 31) & ~31, false);
-          for (int i = 0; i < w.n; ++i, ++g) {
+          // each half of the columns on its own: its warps free it on their own
+          const int n_half = ((n_rows + 31) & ~31) / 2;
+          const uint32_t idesc = idesc_bf16_f32(BN, n_half, false);
+          for (int i = 0; ok && i < w.n; ++i, ++g) {
             const int s = i & 1;
             const uint32_t st = g % kStages;
             if (!(ok = wait(bar(W_FULL + st), (g / kStages) & 1))) break;
-            if (used[s] > 0 && !(ok = wait(bar(W_SEMPTY + s), (used[s] - 1) & 1))) break;
-            ++used[s];
-            tc_fence_after();
             const uint32_t ka = sbase + OFF_RING + st * kTileBytes;
+            for (int half = 0; half < 2; ++half) {
+              if (used[s] > 0 && !(ok = wait(bar(W_SEMPTY + 2 * s + half), (used[s] - 1) & 1))) break;
+              tc_fence_after();
+              const uint32_t d = tmem + s * 256 + half * n_half, qa = sbase + OFF_Q + half * n_half * 128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t c = (k & 3) * 32;
-              mma_ss(tmem + s * 256, smem_desc_sw128(ka + (k >> 2) * kHalfBytes + c, 16, 1024),
-                     smem_desc_sw128(sbase + OFF_Q + (k >> 2) * kQHalfBytes + c, 16, 1024), idesc, k > 0 ? 1u : 0u);
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t c = (k & 3) * 32;
+                mma_ss(d, smem_desc_sw128(ka + (k >> 2) * kHalfBytes + c, 16, 1024),
+                       smem_desc_sw128(qa + (k >> 2) * kQHalfBytes + c, 16, 1024), idesc, k > 0 ? 1u : 0u);
+              }
+              // S - M first, as an exact difference of like numbers, then - log l
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma_ss(d, smem_desc_noswz(sbase + OFF_ONES, 128, 256),
+                       smem_desc_noswz(sbase + OFF_BIAS + k * kRowBlock * 32 + half * n_half * 32, 128, 256), idesc, 1u);
+              mma_commit(bar(W_SFULL + 2 * s + half));
             }
-            // S - M first, as an exact difference of like numbers, then - log l
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma_ss(tmem + s * 256, smem_desc_noswz(sbase + OFF_ONES, 128, 256),
-                     smem_desc_noswz(sbase + OFF_BIAS + k * kRowBlock * 32, 128, 256), idesc, 1u);
-            mma_commit(bar(W_SFULL + s));
+            if (!ok) break;
+            ++used[s];
             mma_commit(bar(W_EMPTY + st));
           }
         }
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
           const bool live = slot < slots;
           float old = 0.f;
           if (live && !upper) old = rb > 0 ? w_out[slot] : slot < w.len ? w_in[slot] : 0.f;
-          if (!(ok = wait(bar(W_SFULL + buf), n_s & 1))) break;
+          if (!(ok = wait(bar(W_SFULL + 2 * buf + upper), n_s & 1))) break;
           ++n_s;
           tc_fence_after();
           const int d = slot - w.len;                // drafted token of the slot
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
           else add_all(std::false_type{});
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(W_SEMPTY + buf));
+          if (lane == 0) mbar_arrive(bar(W_SEMPTY + 2 * buf + upper));
           float a0, a1;
           unpk2(add2(acc[0], acc[1]), a0, a1);
           // the lower columns' warp adds the upper columns' sums and writes
