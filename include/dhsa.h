@@ -426,7 +426,9 @@ int dhsa_rotary_qkv(const void* Q, const int64_t* q_strides, const void* K, cons
  *    left as they were. lengths[b] outside [0, cap] and n_draft[b] outside
  *    [0, T] or past the capacity are clamped (DHSA_DEVFLAG_BAD_CACHE); a
  *    parent outside [-1, t) is taken as -1 (DHSA_DEVFLAG_BAD_TREE).
- *    V rows of cached and drafted tokens must be finite.
+ *    V rows of cached and drafted tokens must be finite. The probabilities
+ *    enter the PV product rounded to bf16; the denominators, lse and the
+ *    weights add them in fp32. O overlaps no input (O == Q is refused).
  *    Results do not depend on what else runs: no atomics on values, one order
  *    of sums for given lengths. workspace: dhsa_tree_attn_workspace_size(B, Hq,
  *    Hkv, T, cap, weight != NULL) bytes; it needs no initial contents. Calls that share a

@@ -444,7 +444,7 @@ int dhsa_tree_attn(const void* Q, const void* K, const int64_t* k_strides, const
                    const float* weight, float* weight_out, void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_cache(B, Hkv, cap, head_dim);
   if (st != DHSA_OK) return st;
-  if (!Q || !K || !V || !lengths || !O || !weight != !weight_out) return DHSA_ERR_INVALID_ARG;
+  if (!Q || !K || !V || !lengths || !O || O == Q || !weight != !weight_out) return DHSA_ERR_INVALID_ARG;
   if (Hq <= 0 || Hq % Hkv != 0 || T <= 0) return DHSA_ERR_INVALID_ARG;
   if ((long long)B * Hq * T > 0x7fffffffLL) return DHSA_ERR_INVALID_ARG;
   if (T > tree_max_drafts() || Hq / Hkv > tree_max_group()) return DHSA_ERR_UNSUPPORTED;

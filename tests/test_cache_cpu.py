@@ -58,11 +58,11 @@ TREE = ("Q K ks V vs B Hq Hkv T cap d lengths parents n_draft scale O lse w wo w
     (dict(Hq=2 * 65), UNS), (dict(d=96), UNS), (dict(cap=0), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV),
     (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(K=FAKE + 2), INV),
     (dict(ks=_strides(1280, 128, 64)), INV), (dict(vs=_strides(1280, 132, 256)), INV), (dict(ws=None), WS),
-    (dict(bytes=16), WS), (dict(ws=FAKE + 4), WS),
+    (dict(bytes=16), WS), (dict(ws=FAKE + 4), WS), (dict(O=FAKE), INV),
 ])
 def test_tree_refusals(lib, change, want):
     ok = dict(Q=FAKE, K=FAKE, ks=None, V=FAKE, vs=None, B=2, Hq=4, Hkv=2, T=5, cap=50, d=128, lengths=FAKE,
-              parents=None, n_draft=None, scale=0.1, O=FAKE, lse=None, w=None, wo=None, ws=FAKE,
+              parents=None, n_draft=None, scale=0.1, O=FAKE + 4096, lse=None, w=None, wo=None, ws=FAKE,
               bytes=lib.dhsa_tree_attn_workspace_size(2, 4, 2, 5, 50, 0), stream=None)
     assert _call(lib.dhsa_tree_attn, TREE, ok, **change) == want
 

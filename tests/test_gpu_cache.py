@@ -576,3 +576,102 @@ def test_evict_more_slots_than_a_cluster_holds_keys_for(lib):
     rng = np.random.default_rng(33)
     cap = 16 * 48 * 1024 + 7000
     _check_evict(lib, rng, 1, 1, cap, [cap - 5], 900, n_draft=[5], accept=[0b10011], sinks=2, recent=5)
+
+
+SPLIT = [  # as TREE, with caches long enough that several CTAs share an item
+    (1, 4, 1, 1, [1100], [1], False, True, {"cap": 1101}),                    # a few rows, by items
+    (1, 40, 1, 1, [2000], [1], False, True, {}),                              # 40 rows: K is read again
+    (2, 8, 1, 9, [1500, 1029], [9, 4], True, True, {}),                       # 72 rows: both lane halves
+    (1, 16, 2, 16, [2300], [16], True, True, {"slot_major": True}),           # 128 rows
+    (3, 8, 2, 40, [1300, 0, 1290], [40, 0, 33], True, True, {"in_place": True}),   # 160 rows: two query tiles
+    (1, 8, 1, 64, [1700], [64], False, True, {}),                             # 512 rows: two query blocks
+    (40, 8, 4, 2, [1200 - 29 * b for b in range(40)], [b % 3 for b in range(40)], True, True, {"cap": 1210}),
+    (40, 2, 1, 1, [1900] + [5] * 39, [1] * 40, False, True, {}),              # one long, many short
+    (200, 1, 1, 1, [1500 if b in (3, 150) else 7 * b for b in range(200)], [int(b in (3, 150)) for b in range(200)],
+     False, True, {"cap": 1600}),                                             # most sequences have no new token
+    (150, 4, 1, 3, [(37 * b) % 1400 for b in range(150)], [3] * 150, True, False, {"cap": 1410}),
+]
+
+
+@needs_gpu
+@pytest.mark.parametrize("case", SPLIT, ids=[f"{i}-" + "x".join(map(str, c[:4])) for i, c in enumerate(SPLIT)])
+def test_tree_attn_split(lib, case):
+    B, Hq, Hkv, T, lengths, drafts, tree, weights, opt = case
+    _check_tree(lib, np.random.default_rng(sum(lengths) + T), B, Hq, Hkv, T, lengths, drafts, tree, weights, **opt)
+
+
+@needs_gpu
+def test_tree_attn_garbage_behind_the_rows_and_slots(lib):
+    """Rows of missing tokens hold NaN queries, slots behind the last one NaN
+    keys and values, weights of unused slots NaN: none of it shows."""
+    rng = np.random.default_rng(24)
+    for G, T, n in ((2, 4, 300), (8, 30, 2000)):
+        cap = n + 77
+        Q, K, V = _bf(rng, 2, G, T, D), _bf(rng, 2, 1, cap, D), _bf(rng, 2, 1, cap, D)
+        nd = [T, T // 2]
+        clean = torch.zeros(2, 1, cap, device="cuda")
+        ref, wref = torch.zeros_like(Q), torch.zeros_like(clean)
+        lib.tree_attn(Q, K, V, _i32([n, n - 200]), n_draft=_i32(nd), weight=clean, weight_out=wref, out=ref)
+        nan = float("nan")
+        w = clean.clone()
+        Q[1, :, nd[1]:] = nan
+        for b, end in enumerate((n + nd[0], n - 200 + nd[1])):
+            K[b, :, end:] = nan
+            V[b, :, end:] = nan
+            w[b, :, end - nd[b]:] = nan
+        got, wgot = torch.zeros_like(Q), torch.zeros_like(w)
+        lib.tree_attn(Q, K, V, _i32([n, n - 200]), n_draft=_i32(nd), weight=w, weight_out=wgot, out=got)
+        assert torch.equal(got, ref) and torch.equal(wgot, wref)
+
+
+@needs_gpu
+def test_streamed_and_graphed_prefill_with_rotary_positions(lib):
+    from long_context_prefill_dhsa_b200 import inputs as I
+    w = I.custom(B=1, Hq=4, Hkv=2, L=500, lo=20, hi=120, k=3, wid=901)
+    d = I.make_inputs(w)
+    off, nc = (torch.from_numpy(np.ascontiguousarray(d[x])).cuda() for x in ("off", "n_chunks"))
+    f = torch.from_numpy(10000.0 ** (-np.arange(64) / 64)).cuda()
+    mk = lambda: lib.DHSAPrefill(1, 4, 2, 500, off, nc, w.k, inv_freq=f, interleaved=True)
+    rng = np.random.default_rng(43)
+    steps = [[_bf(rng, 1, H, 500, D) for H in (4, 2, 2)] for _ in range(3)]
+    want = [mk().run(*s).clone() for s in steps]
+    streamed = lib.HostStreamedPrefill(mk())
+    host = [[x.cpu().pin_memory() for x in s] + [torch.empty(1, 4, 500, D, dtype=torch.bfloat16).pin_memory()]
+            for s in steps]
+    torch.cuda.synchronize()
+    for h in host:
+        streamed.submit(*h)
+    streamed.synchronize()
+    graphed = lib.GraphedPrefill(mk(), *[x.clone() for x in steps[0]])
+    for s, h, o in zip(steps, host, want):
+        for dst, src in zip((graphed.Q, graphed.K, graphed.V), s):
+            dst.copy_(src)
+        assert torch.equal(graphed.replay(), o) and torch.equal(h[3].cuda(), o)
+
+
+@needs_gpu
+def test_calls_on_a_side_stream_and_with_a_callers_workspace(lib):
+    """A workspace full of NaN, a side stream: the same bits as the plain call."""
+    rng = np.random.default_rng(44)
+    B, Hq, Hkv, T, cap = 2, 8, 2, 3, 5000
+    Q, K, V = _bf(rng, B, Hq, T, D), _bf(rng, B, Hkv, cap, D), _bf(rng, B, Hkv, cap, D)
+    n, w = _i32([4990, 2000]), torch.rand(B, Hkv, cap, device="cuda")
+    wo = torch.zeros_like(w)
+    want = lib.tree_attn(Q, K, V, n, weight=w, weight_out=wo)
+    size = lib.load().dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, 1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        got_w = torch.zeros_like(w)
+        got = lib.tree_attn(Q, K, V, n, weight=w, weight_out=got_w, workspace=ws)
+    s.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_w, wo)
+    with pytest.raises(lib.DHSAError):
+        lib.tree_attn(Q, K, V, n, weight=w, workspace=ws[: size - 256])
+    with pytest.raises(ValueError):
+        lib.tree_attn(Q, K, V, n.cpu(), weight=w)
+    with pytest.raises(ValueError):
+        lib.tree_attn(Q, K[:, :, :, ::1].transpose(2, 3), V, n)
+    with pytest.raises(lib.DHSAError):
+        lib.tree_attn(Q, K, V, n, out=Q)
