@@ -121,32 +121,47 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
   const int w0 = blk0 + warp * per_warp, w1 = min(w0 + per_warp, n_all);
 
   auto is_cand = [&](int s) { return s < sl.len || ((bits >> (s - sl.len)) & 1ull); };
-  auto make_key = [&](int s) -> uint32_t {
-    const int q = pos_in[s];
-    const float w = w_in[s];
+  auto key_from = [&](int s, float w, int q) -> uint32_t {
     return !is_cand(s) ? 0u : (q < p.sinks || q >= held_from) ? 0xFFFFFFFFu : weight_key(w);
+  };
+  // What stays where it is, and the index of it: written for every slot below
+  // m as it is first read; the holes among them are written again at the end.
+  int32_t* idx_row = p.index ? p.index + (long long)bh * p.index_cols : nullptr;
+  float* w_out = p.weight_out + row;
+  int32_t* pos_out = p.pos_out + row;
+  const bool copy_w = w_out != w_in, copy_pos = pos_out != pos_in;
+  auto keep_in_place = [&](int s, float w, int q) {
+    if (copy_w) w_out[s] = w;
+    if (copy_pos) pos_out[s] = q;
+    if (idx_row) idx_row[s] = s;
   };
 
   const bool all = m == n_cand;            // every candidate stays: no ranking
   uint32_t cut = 0;                        // the m-th largest key
   uint32_t ties = 0;                       // how many of the slots with that key stay
-  auto key_of = [&](int s) { return s - blk0 < p.keys_held ? keys[s - blk0] : make_key(s); };
+  auto key_of = [&](int s) { return s - blk0 < p.keys_held ? keys[s - blk0] : key_from(s, w_in[s], pos_in[s]); };
   if (!all) {
     for (int i = tid; i < kRounds * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
     for (int s0 = w0; s0 < w1; s0 += 32 * kBatch) {
-      uint32_t k[kBatch];
+      float w[kBatch];
+      int q[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int s = s0 + 32 * u + lane;
-        k[u] = s < w1 ? make_key(s) : 0u;
+        if (s < w1) {
+          w[u] = w_in[s];
+          q[u] = pos_in[s];
+        }
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int s = s0 + 32 * u + lane;
-        if (s0 + 32 * u >= w1) break;
-        if (s < w1 && s - blk0 < p.keys_held) keys[s - blk0] = k[u];
-        if (s < w1) atomicAdd(&sh.hist[0][k[u] >> 24], 1u);
+        if (s >= w1) break;
+        const uint32_t k = key_from(s, w[u], q[u]);
+        if (s - blk0 < p.keys_held) keys[s - blk0] = k;
+        atomicAdd(&sh.hist[0][k >> 24], 1u);
+        if (s < m) keep_in_place(s, w[u], q[u]);
       }
     }
     uint32_t left = (uint32_t)m;
@@ -256,46 +271,36 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
     return yes;
   };
 
-  // the lists, and what stays where it is
+  // the lists
   int32_t* hole_list = p.lists + row;
   int32_t* src_list = hole_list + p.cap / 2;   // min(m, n_all - m) <= cap / 2 rows move
-  int32_t* idx_row = p.index ? p.index + (long long)bh * p.index_cols : nullptr;
-  float* w_out = p.weight_out + row;
-  int32_t* pos_out = p.pos_out + row;
-  const bool copy_w = w_out != w_in, copy_pos = pos_out != pos_in;
-  for (int s0 = w0; s0 < w1; s0 += 32 * kBatch) {
-    uint32_t here = 0;                 // bit u: slot s0 + 32 u + lane stays where it is
+#pragma unroll 2
+  for (int s0 = w0; s0 < w1; s0 += 32) {
+    const int s = s0 + lane;
+    const bool yes = stays(s);
+    const bool hole = s < m && s < w1 && !yes, src = s >= m && yes;
+    const uint32_t hb = __ballot_sync(0xffffffffu, hole), sb = __ballot_sync(0xffffffffu, src);
+    if (hole) hole_list[hole_at + __popc(hb & lt)] = s;
+    if (src) src_list[src_at + __popc(sb & lt)] = s;
+    hole_at += __popc(hb);
+    src_at += __popc(sb);
+  }
+  if (all && (copy_w || copy_pos || idx_row)) {
+    for (int s0 = rank * kEvThreads + tid; s0 < m; s0 += C * kEvThreads * kBatch) {
+      float w[kBatch];
+      int q[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int s = s0 + 32 * u + lane;
-      if (s0 + 32 * u >= w1) break;
-      const bool yes = stays(s);
-      const bool hole = s < m && s < w1 && !yes, src = s >= m && yes;
-      const uint32_t hb = __ballot_sync(0xffffffffu, hole), sb = __ballot_sync(0xffffffffu, src);
-      if (hole) hole_list[hole_at + __popc(hb & lt)] = s;
-      if (src) src_list[src_at + __popc(sb & lt)] = s;
-      hole_at += __popc(hb);
-      src_at += __popc(sb);
-      if (yes && s < m) here |= 1u << u;
-    }
-    if (s0 >= m || !(copy_w || copy_pos || idx_row)) continue;
-    float wv[kBatch];
-    int32_t pv[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int s = s0 + 32 * u + lane;
-      if ((here >> u) & 1) {
-        wv[u] = w_in[s];
-        pv[u] = pos_in[s];
+      for (int u = 0; u < kBatch; ++u) {
+        const int s = s0 + u * C * kEvThreads;
+        if (s < m) {
+          w[u] = w_in[s];
+          q[u] = pos_in[s];
+        }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int s = s0 + 32 * u + lane;
-      if ((here >> u) & 1) {
-        if (idx_row) idx_row[s] = s;
-        if (copy_w) w_out[s] = wv[u];
-        if (copy_pos) pos_out[s] = pv[u];
+      for (int u = 0; u < kBatch; ++u) {
+        const int s = s0 + u * C * kEvThreads;
+        if (s < m) keep_in_place(s, w[u], q[u]);
       }
     }
   }
