@@ -42,6 +42,7 @@ constexpr int kMaxScoreRows = 32;   // rows of a head up to which the attention 
 constexpr int kMaxGrid = 160;    // CTAs (one per SM) the workspace is sized for
 
 constexpr int kTileSlots = 128;  // slots of a key tile
+constexpr int kTileRows = 128;   // query rows of a query tile
 constexpr uint32_t kTmemCols = 512;
 
 // key tiles of each item of a sequence, and the item's length on the line

@@ -41,7 +41,8 @@
 
 namespace dhsa {
 
-int launch_tree_weight_scores(const TreeParams& p, cudaStream_t stream);
+int launch_tree_join(const TreeParams& p, cudaStream_t stream);
+int launch_tree_join_weights(const TreeParams& p, cudaStream_t stream);
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream);
 
 namespace {
@@ -88,7 +89,7 @@ constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
 constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;   // slack for aligning the base
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 static_assert(sizeof(Line) % 8 == 0, "alignment");
-static_assert(BN == kTileSlots, "the line is cut into these tiles");
+static_assert(BN == kTileSlots && BM == kTileRows, "the line is cut into these tiles");
 
 constexpr int W_PRODUCER = 0, W_MMA = 1, W_SOFTMAX0 = 4;
 
@@ -562,78 +563,6 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
   tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of a row that several CTAs share: O = sum_i f_i O_i /
-// sum_i f_i l_i, f_i = exp(scale (m_i - M)). One block of one warp per row, 16
-// bytes a lane. (Blocks of four warps took 1 to 3 us more, and so did letting
-// them start while the attention runs: they then crowd on the SMs that are
-// free first.)
-__global__ void __launch_bounds__(32) tree_combine_kernel(const TreeParams p) {
-  __shared__ float f[kMaxGrid];
-  __shared__ int at[kMaxGrid];
-  const int lane = threadIdx.x;
-  launch_dependents();
-  const long long row = blockIdx.x;
-  const int r = (int)(row % p.rows), bh = (int)(row / p.rows);
-  const int b = bh / p.Hkv;
-  const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-  const int wide = p.rows > BM ? 2 : 1;              // query tiles of a block
-  const int block = r / (wide * BM), tile = r / BM % wide, tr = r % BM;
-  const int item = bh * p.blocks + block;
-  // no kernel of the chain ends before the one it follows
-  wait_for_predecessors();
-  if (r % p.T >= s.draft) return;
-  const int2 span = p.span[item];
-  const int c0 = span.x, c1 = span.y;
-  if (c0 == c1) return;                              // one CTA had the whole item and wrote its rows
-  int n = 0;
-  float mx = -INFINITY;
-  for (int x0 = c0; x0 <= c1; x0 += 32) {
-    const int c = x0 + lane;
-    const bool has = c <= c1;
-    const int slot = (c + item) * wide + tile;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (has) ml = p.part_ml[(long long)slot * p.row_cap + tr];
-    const uint32_t v = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
-    if (ml.x != -INFINITY) {
-      const int q = n + __popc(v & ((1u << lane) - 1));
-      f[q] = ml.x;
-      at[q] = slot;
-    }
-    n += __popc(v);
-    mx = fmaxf(mx, ml.x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  __syncwarp();
-  float l = 0.f;
-  for (int q = lane; q < n; q += 32) {
-    const float k = fast_exp2((f[q] - mx) * p.scale_log2);
-    l += k * p.part_ml[(long long)at[q] * p.row_cap + tr].y;
-    f[q] = k;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  __syncwarp();
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int q = 0; q < n; ++q) {
-    const float k = f[q];
-    const float4 v =
-        *reinterpret_cast<const float4*>(p.part_o + ((long long)at[q] * p.row_cap + tr) * kHeadDim + 4 * lane);
-    o.x += k * v.x;
-    o.y += k * v.y;
-    o.z += k * v.z;
-    o.w += k * v.w;
-  }
-  const float g = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(p.O + row * kHeadDim + 4 * lane) =
-      make_uint2(pack_bf16x2(o.x * g, o.y * g), pack_bf16x2(o.z * g, o.w * g));
-  if (lane == 0) {
-    if (p.lse) p.lse[row] = mx * p.scale + logf(l);
-    if (p.row_stat) p.row_stat[row] = make_float2(mx, 1.f / l);
-  }
-}
-
 struct Plan {
   int rows, wide, blocks, row_cap, score_cap;
   bool whole, scores;
@@ -725,11 +654,12 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.status = status;
   kernel<<<p.grid, block_threads(halves), kSmemAlloc, stream>>>(maps, p);
   int st = launch_status();
-  if (st == DHSA_OK && !q.whole)
-    st = launch_after(tree_combine_kernel, dim3((unsigned)((long long)B * Hkv * q.rows)), dim3(32), 0, stream, p);
-  if (st == DHSA_OK && weight_out && q.scores) {
-    st = launch_tree_weight_scores(p, stream);
-  } else if (st == DHSA_OK && weight_out) {
+  if (st == DHSA_OK && q.scores) {
+    st = launch_tree_join_weights(p, stream);
+  } else if (st == DHSA_OK && !q.whole) {
+    st = launch_tree_join(p, stream);
+  }
+  if (st == DHSA_OK && weight_out && !q.scores) {
     p.whole = false;
     p.every = true;                   // weights without new tokens are passed on
     p.blocks = 1;                     // one walk over the keys for all rows of a head

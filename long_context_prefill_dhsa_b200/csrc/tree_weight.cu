@@ -347,48 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   tmem_dealloc(tmem, kTmemCols);
 }
 
-// The same from scores that the attention kept, for few rows: 8 bytes per slot
-// and row instead of K's 256, nothing to compute but the exponentials.
-constexpr int kSlotThreads = 256, kSlotsEach = 4;
-__global__ void __launch_bounds__(kSlotThreads) tree_weight_scores_kernel(const TreeParams p) {
-  __shared__ float2 stat[kMaxScoreRows];
-  const int parts = (p.cap + kSlotThreads * kSlotsEach - 1) / (kSlotThreads * kSlotsEach);
-  const int bh = blockIdx.x / parts, b = bh / p.Hkv, h = bh % p.Hkv;
-  const SeqLen s = seq_len(p.lengths, p.n_draft, p.T, b, p.T, p.cap);
-  const int block0 = blockIdx.x % parts * (kSlotThreads * kSlotsEach), first = block0 + threadIdx.x;
-  if (block0 >= s.len + s.draft) {
-    wait_for_predecessors();       // no kernel of the chain ends before the one it follows
-    return;
-  }
-  float old[kSlotsEach];
-#pragma unroll
-  for (int k = 0; k < kSlotsEach; ++k) {
-    const int slot = first + k * kSlotThreads;
-    old[k] = slot < s.len ? p.weight[(long long)bh * p.cap + slot] : 0.f;
-  }
-  wait_for_predecessors();
-  if (threadIdx.x < p.rows) {
-    const bool live = threadIdx.x % p.T < s.draft;
-    stat[threadIdx.x] = live ? p.row_stat[((long long)b * p.Hq + h * p.G) * p.T + threadIdx.x] : make_float2(0.f, 0.f);
-  }
-  __syncthreads();
-  float sum[kSlotsEach] = {0.f, 0.f, 0.f, 0.f};
-  for (int r = 0; r < p.rows; ++r) {
-    const float2 st = stat[r];
-    if (st.y == 0.f) continue;       // a missing token's row
-    const float* row = p.scores + ((long long)bh * p.rows + r) * p.score_cap + first;
-#pragma unroll
-    for (int k = 0; k < kSlotsEach; ++k)
-      if (first + k * kSlotThreads < s.len + s.draft)
-        sum[k] += fast_exp2((row[k * kSlotThreads] - st.x) * p.scale_log2) * st.y;
-  }
-#pragma unroll
-  for (int k = 0; k < kSlotsEach; ++k) {
-    const int slot = first + k * kSlotThreads;
-    if (slot < s.len + s.draft) p.weight_out[(long long)bh * p.cap + slot] = old[k] + sum[k];
-  }
-}
-
 }  // namespace
 
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream) {
@@ -398,11 +356,6 @@ int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t s
   if (e == cudaSuccess) e = allow_smem(tree_weight_kernel, (int)kSmemAlloc, dev, done);
   if (e != cudaSuccess) return cuda_status(e);
   return launch_after(tree_weight_kernel, dim3(p.grid), dim3(kThreads), kSmemAlloc, stream, k, p);
-}
-
-int launch_tree_weight_scores(const TreeParams& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)((long long)ceil_div(p.cap, kSlotThreads * kSlotsEach) * p.B * p.Hkv));
-  return launch_after(tree_weight_scores_kernel, grid, dim3(kSlotThreads), 0, stream, p);
 }
 
 }  // namespace dhsa
