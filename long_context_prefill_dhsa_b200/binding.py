@@ -415,15 +415,18 @@ def sparse_attn_fwd_noalloc(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, o
 # These calls are made once per new token, so their checks are kept cheap: one
 # pass that accepts, and the reasons only for what it does not.
 _raw_stream = torch._C._cuda_getCurrentRawStream     # current stream of a device, as an address
+_Strides = ctypes.c_int64 * 3
 
 
 def _on(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
     """A dense tensor of the call, on the call's device; returns its pointer (None for None)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device \
-            and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _need(t, dtype, shape, name)
     raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
 
@@ -433,12 +436,15 @@ def _rows(t: Optional[torch.Tensor], shape, name: str, device: int):
     returns its pointer and its strides for the library (None when dense)."""
     if t is None:
         return None, None
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device:
-        if t.is_contiguous():
-            return t.data_ptr(), None
-        if t.stride(3) != 1:
-            raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
-        return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device:
+            if t.is_contiguous():
+                return t.data_ptr(), None
+            if t.stride(3) != 1:
+                raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
+            return t.data_ptr(), _Strides(*t.stride()[:3])
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != torch.bfloat16:
@@ -498,7 +504,7 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
     (slots None: t); missing outputs are allocated with T rows. Rows
     t >= n_new[b] are left alone. transpose=True applies the transposed
     rotation (its gradient). Returns (Q_out, K_out, V_out)."""
-    ref = next((x for x in (Q, K, V) if x is not None), None)
+    ref = Q if Q is not None else K if K is not None else V
     if ref is None:
         raise ValueError("rotary_qkv: Q, K and V are all None")
     device = _call_device(ref, "Q" if Q is not None else "K" if K is not None else "V")
@@ -513,9 +519,8 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
     q, qs = _rows(Q, (B, Hq, T, d), "Q", device)
     k, ks = _rows(K, (B, Hkv, T, d), "K", device)
     v, vs = _rows(V, (B, Hkv, T, d), "V", device)
-    for x, o, name in ((Q, Q_out, "Q_out"), (K, K_out, "K_out"), (V, V_out, "V_out")):
-        if x is None and o is not None:
-            raise ValueError(f"{name}: given without its input")
+    if (Q is None and Q_out is not None) or (K is None and K_out is not None) or (V is None and V_out is not None):
+        raise ValueError("rotary_qkv: an output is given without its input")
     if Q is not None and Q_out is None:
         Q_out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=device)
     cap = K_out.shape[2] if K_out is not None else V_out.shape[2] if V_out is not None else T
