@@ -98,13 +98,16 @@ template <int NQT, int HALVES>
 __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(const __grid_constant__ TreeMaps maps,
                                                                 const TreeParams p) {
   constexpr int kThreads = block_threads(HALVES), kStreamWarps = 4 * HALVES;
-  constexpr int NST = (kSmemData - NQT * kTileBytes) / kKvBytes;   // ring stages
+  // rows of the MMAs: with 64, their D lies in the first 16 lanes of each quarter
+  constexpr int MQ = 64 * HALVES, kQBits = 5 + HALVES, kLanes = 16 * HALVES;
+  constexpr uint32_t kQHalf = MQ * 128, kQTile = 2 * kQHalf;
+  constexpr int NST = (kSmemData - NQT * kQTile) / kKvBytes;   // ring stages
   constexpr int kAhead = 2 / NQT;   // tiles whose scores are computed ahead: one S for each of two streams
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t ring = sbase + NQT * kTileBytes;
+  const uint32_t ring = sbase + NQT * kQTile;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   Line* line = reinterpret_cast<Line*>(smem + OFF_LINE);
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
@@ -190,16 +193,16 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
   } else if (warp == W_MMA) {
     // The whole warp runs the loop converged and lane 0 issues.
     const uint32_t on = lane == 0;
-    const uint32_t idesc_qk = idesc_bf16_f32(BM, BN, false), idesc_pv = idesc_bf16_f32(BM, kHeadDim, true);
+    const uint32_t idesc_qk = idesc_bf16_f32(MQ, BN, false), idesc_pv = idesc_bf16_f32(MQ, kHeadDim, true);
     constexpr uint32_t kHi = desc_hi_sw128(1024);
     const uint32_t q_lo = desc_lo_sw128(sbase, 16), k_lo = desc_lo_sw128(ring, 16);
     const uint32_t v_lo = desc_lo_sw128(ring, kKvHalfBytes);
     uint32_t g = 0, n_piece = 0, p_phase = 0;    // p_phase: parity of P's barriers, a bit for each stream
     auto qk = [&](int s, uint32_t stage) {      // S = Q K^T
-      const uint32_t qa = q_lo + (NQT == 2 ? s * (kTileBytes >> 4) : 0), ka = k_lo + stage * (kKvBytes >> 4);
+      const uint32_t qa = q_lo + (NQT == 2 ? s * (kQTile >> 4) : 0), ka = k_lo + stage * (kKvBytes >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        mma_ss_lo(on, tmem + s * 128, qa + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+        mma_ss_lo(on, tmem + s * 128, qa + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4),
                   ka + (((k >> 2) * kKvHalfBytes + (k & 3) * 32) >> 4), kHi, idesc_qk, k > 0 ? 1u : 0u);
       mma_commit_on(on, bar(B_SFULL + s));
     };
@@ -278,19 +281,19 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
       const __nv_bfloat16* q_head = p.Q + ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T * kHeadDim;
       const int row0 = w.block * (NQT == 2 ? 2 * BM : BM);      // first row of the block
       const int ch = lane & 15;
-      constexpr int kEach = NQT * BM / (2 * kStreamWarps) / 2;   // 16-byte words of a lane
+      constexpr int kEach = NQT * MQ / (2 * kStreamWarps) / 2;   // 16-byte words of a lane
       uint4 v[kEach];
 #pragma unroll
       for (int it = 0; it < kEach; ++it) {
-        const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & 127;
-        const int r = row0 + (at >> 7) * BM + 4 * (L & 31) + (L >> 5);
+        const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & (MQ - 1);
+        const int r = row0 + (at >> kQBits) * BM + 4 * (L & (kLanes - 1)) + (L >> (kQBits - 2));
         v[it] = make_uint4(0, 0, 0, 0);
         if (r < p.rows) v[it] = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
       }
 #pragma unroll
       for (int it = 0; it < kEach; ++it) {
-        const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & 127;
-        *reinterpret_cast<uint4*>(smem + (at >> 7) * kTileBytes + (ch >> 3) * kHalfBytes + L * 128 +
+        const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & (MQ - 1);
+        *reinterpret_cast<uint4*>(smem + (at >> kQBits) * kQTile + (ch >> 3) * kQHalf + L * 128 +
                                   (((ch & 7) ^ (L & 7)) << 4)) = v[it];
       }
       fence_proxy_async_smem();
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
         if (k0 + BN > slots && (NQT == 1 || stream == 0)) {
           const uint32_t q = g + 2 * w.n - 1;      // the item's last tile is the piece's last load
           if (!(ok = wait(bar(B_FULL + q % NST), (q / NST) & 1))) break;
-          unsigned char* v = smem + NQT * kTileBytes + (q % NST) * kKvBytes;
+          unsigned char* v = smem + NQT * kQTile + (q % NST) * kKvBytes;
           for (int x = (slots - k0) * 16 + (hf * 4 + quarter) * 32 + lane; x < BN * 16; x += 32 * kStreamWarps)
             *reinterpret_cast<uint4*>(v + (x & 1) * kKvHalfBytes + (x >> 1) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
