@@ -531,6 +531,8 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
     qo = _on(Q_out, torch.bfloat16, (B, Hq, T, d), "Q_out", device)
     ko, kos = _rows(K_out, (B, Hkv, cap, d), "K_out", device)
     vo, vos = _rows(V_out, (B, Hkv, cap, d), "V_out", device)
+    if not isinstance(inv_freq, torch.Tensor):
+        raise TypeError("inv_freq: expected a torch.Tensor")
     if positions is not None and start is not None:
         raise ValueError("rotary_qkv: positions and start exclude each other")
     _check(load().dhsa_rotary_qkv(

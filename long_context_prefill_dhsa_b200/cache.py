@@ -69,13 +69,15 @@ class KVCache:
     K, V [B,Hkv,cap,128], weight (fp32) and pos (int32) [B,Hkv,cap], lengths
     and next_pos (int32 [B]) are the state; every call runs on the current
     stream and none synchronises. Not for use from two streams at once.
+    Caches used one after the other (the layers of a model) can share one
+    `workspace` (uint8, workspace_size bytes). Tokens that lead past `cap` are
+    not stored and raise DHSA_DEVFLAG_BAD_CACHE (binding.check_device_status).
     """
 
     def __init__(self, B: int, Hq: int, Hkv: int, cap: int, inv_freq: torch.Tensor, interleaved: bool = False,
                  rotary_factor: float = 1.0, softmax_scale: Optional[float] = None, track_weight: bool = True,
-                 sinks: int = 0, recent: int = 0, device="cuda"):
+                 sinks: int = 0, recent: int = 0, workspace: Optional[torch.Tensor] = None, device="cuda"):
         dev = torch.device(device)
-        lib = binding.load()
         self.B, self.Hq, self.Hkv, self.cap = B, Hq, Hkv, cap
         self.inv_freq, self.interleaved, self.rotary_factor = inv_freq, interleaved, rotary_factor
         self.scale, self.track_weight, self.sinks, self.recent = softmax_scale, track_weight, sinks, recent
@@ -87,14 +89,22 @@ class KVCache:
         self.lengths = torch.zeros(B, dtype=torch.int32, device=dev)
         self._lengths_next = torch.zeros_like(self.lengths)
         self.next_pos = torch.zeros_like(self.lengths)
-        # what a step needs depends on its number of tokens, and not only upwards
-        self._ws = torch.empty(max(
-            lib.dhsa_cache_evict_workspace_size(B, Hkv, cap),
-            *(lib.dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, track_weight)
-              for T in range(1, lib.dhsa_tree_max_drafts() + 1))), dtype=torch.uint8, device=dev)
-        self._bits = torch.arange(lib.dhsa_tree_max_drafts(), dtype=torch.int64, device=dev)
+        self._ws = workspace if workspace is not None else torch.empty(
+            self.workspace_size(B, Hq, Hkv, cap, track_weight), dtype=torch.uint8, device=dev)
+        self._bits = torch.arange(binding.tree_max_drafts(), dtype=torch.int64, device=dev)
         self._prompt: Optional[int] = None      # tokens of a prompt that nothing has followed yet
         self._arange = torch.arange(cap, dtype=torch.int32, device=dev)
+
+    @staticmethod
+    def workspace_size(B: int, Hq: int, Hkv: int, cap: int, track_weight: bool = True) -> int:
+        """Bytes of workspace that steps of any number of tokens need. What a
+        step needs depends on its number of tokens, and not only upwards: up
+        to 32 rows (query heads of a kv head x tokens) its scores are kept,
+        4 bytes per row and slot."""
+        lib = binding.load()
+        return max(lib.dhsa_cache_evict_workspace_size(B, Hkv, cap),
+                   *(lib.dhsa_tree_attn_workspace_size(B, Hq, Hkv, T, cap, track_weight)
+                     for T in range(1, lib.dhsa_tree_max_drafts() + 1)))
 
     def fill(self, K: torch.Tensor, V: torch.Tensor):
         """Start over from a prompt: K (rotated) and V [B,Hkv,L,128] take slots 0 .. L-1."""

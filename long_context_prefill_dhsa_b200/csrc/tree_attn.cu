@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     const int cq = lane & 3;
     const uint32_t tS = tmem + ((uint32_t)(quarter * 32 + hf * 16) << 16) + stream * 128;
     const uint32_t tO = tS + 256;
-    const float c = p.scale_log2, raise = kRaise / c;
+    const float c = p.scale_log2, raise = fminf(kRaise / c, 3e38f);   // finite, so that -inf + raise is -inf
     const uint64_t c2 = pk2(c, c);
     // written by every softmax warp with the same values
     uint64_t* see = reinterpret_cast<uint64_t*>(smem + OFF_SEE);

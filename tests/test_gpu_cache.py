@@ -675,3 +675,43 @@ def test_calls_on_a_side_stream_and_with_a_callers_workspace(lib):
         lib.tree_attn(Q, K[:, :, :, ::1].transpose(2, 3), V, n)
     with pytest.raises(lib.DHSAError):
         lib.tree_attn(Q, K, V, n, out=Q)
+
+
+@needs_gpu
+def test_layers_share_a_workspace(lib):
+    """Two caches with one workspace, stepped in turn, against two with their own."""
+    from long_context_prefill_dhsa_b200 import cache
+    rng = np.random.default_rng(45)
+    B, Hq, Hkv, cap = 2, 8, 2, 1500
+    ws = torch.empty(cache.KVCache.workspace_size(B, Hq, Hkv, cap), dtype=torch.uint8, device="cuda")
+    pairs = [[_cache(B, Hq, Hkv, cap, recent=4, workspace=w) for _ in range(2)] for w in (ws, None)]
+    prompts = [[_bf(rng, B, Hkv, 1400, D) for _ in range(2)] for _ in range(2)]
+    for layers in pairs:
+        for c, x in zip(layers, prompts):
+            c.fill(*x)
+    for T in (1, 5, 40):
+        x = [[_bf(rng, B, H, T, D) for H in (Hq, Hkv, Hkv)] for _ in range(2)]
+        outs = []
+        for layers in pairs:
+            for c, (q, k, v) in zip(layers, x):
+                outs.append(c.attend(c.extend(q, k, v)))
+                c.commit(_i32([T, T]), keep=1398)
+        assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    for a, b in zip(*pairs):
+        assert torch.equal(a.K, b.K) and torch.equal(a.weight, b.weight) and torch.equal(a.pos, b.pos)
+
+
+@needs_gpu
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e30])
+def test_tree_attn_extreme_scales(lib, scale):
+    """A scale so small that every slot weighs the same, one so large that the best slot takes all."""
+    rng = np.random.default_rng(46)
+    n = 700
+    Q, K, V = _bf(rng, 1, 2, 1, D), _bf(rng, 1, 1, n + 1, D), _bf(rng, 1, 1, n + 1, D)
+    out = lib.tree_attn(Q, K, V, _i32([n]), softmax_scale=scale)
+    s = _np(K[0, 0]) @ _np(Q[0, :, 0]).T
+    v = _np(V[0, 0])
+    for h in range(2):
+        want = v.mean(0) if scale < 1 else v[s[:, h].argmax()]
+        tol = U_BF * (np.abs(v).mean(0) + np.abs(want)) * 1.01 if scale < 1 else 0
+        assert np.all(np.abs(_np(out[0, h, 0]) - want) <= tol)
