@@ -38,7 +38,13 @@ using namespace ptx;
 
 constexpr int kMaxDrafts = 64;   // one bit of a 64-bit word each
 constexpr int kMaxGroup = 64;    // query heads of one kv head
-constexpr int kMaxScoreRows = 32;   // rows of a head up to which the attention keeps its scores for the weight pass
+// Rows of a head up to which the attention keeps its scores (4 bytes per row
+// and slot) for the slots' weights; with more rows the weights are computed
+// again from K. Kept against computed again, us, 32/8 heads: one sequence of
+// 131000 slots with 8, 16, 24, 32 rows 104, 119, 134, 150 against 168 to 171;
+// 16 of 4000 to 8000 slots 83, 92, -, 118 against 163 to 166. Each further row
+// adds about 2 us at 128K, so the two meet near 44 rows.
+constexpr int kMaxScoreRows = 32;
 constexpr int kMaxGrid = 160;    // CTAs (one per SM) the workspace is sized for
 
 constexpr int kTileSlots = 128;  // slots of a key tile

@@ -26,8 +26,9 @@ __device__ __forceinline__ RowPieces row_pieces(const TreeParams& p, int bh, int
   q.tile = r / kTileRows % q.wide;
   q.tr = r % kTileRows;
   const int2 span = p.whole ? make_int2(0, 0) : p.span[q.item];
-  q.c0 = span.x;
-  q.c1 = span.y;
+  // (a CTA whose wait ran out leaves its span unwritten: the rows are wrong, and flagged, but stay in range)
+  q.c0 = (int)min((unsigned)span.x, (unsigned)(p.grid - 1));
+  q.c1 = max(q.c0, (int)min((unsigned)span.y, (unsigned)(p.grid - 1)));
   return q;
 }
 
@@ -46,7 +47,7 @@ __device__ __forceinline__ float2 row_denominator(const TreeParams& p, const Row
     const float2 ml = c == q.c0 + lane ? first : p.part_ml[q.at(p, c)];
     const float k = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - mx) * p.scale_log2);
     l += k * ml.y;
-    if (f) f[c - q.c0] = k;
+    f[c - q.c0] = k;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -124,29 +125,65 @@ __global__ void __launch_bounds__(kThreads) tree_join_weights_kernel(const TreeP
   }
   wait_for_predecessors();
   if (block0 >= s.len + s.draft) return;
-  for (int r = warp; r < p.rows; r += kWarps) {
-    float2 st = make_float2(0.f, 0.f);
-    if (r % p.T < s.draft) {
-      const RowPieces q = row_pieces(p, bh, r);
-      if (q.complete()) {
-        st = p.row_stat[(long long)bh * p.rows + r];
-      } else {
-        const float2 ml = row_denominator(p, q, lane, nullptr);
-        st = make_float2(ml.x, 1.f / ml.y);
+  // Few rows are one query tile, so the head is one item; without drafted
+  // tokens there was no item, and `span` has nothing for it. The chains of the
+  // rows' loads run side by side.
+  const int rows = s.draft > 0 ? p.rows : 0;
+  const RowPieces q = rows ? row_pieces(p, bh, 0) : RowPieces{};
+  if (q.complete()) {
+    const int r = threadIdx.x;
+    if (r < rows) stat[r] = r % p.T < s.draft ? p.row_stat[(long long)bh * p.rows + r] : make_float2(0.f, 0.f);
+  } else {
+    constexpr int kEach = kMaxScoreRows / kWarps;
+    float mx[kEach], l[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      mx[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    for (int c0 = q.c0; c0 <= q.c1; c0 += 32) {
+      float2 ml[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = warp + i * kWarps;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (c0 + lane <= q.c1 && r < rows) ml[i] = p.part_ml[q.at(p, c0 + lane) + r];
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        float top = fmaxf(mx[i], ml[i].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // a lane's sum so far is relative to the old reference
+        const float keep = mx[i] == -INFINITY ? 0.f : fast_exp2((mx[i] - top) * p.scale_log2);
+        const float add = ml[i].x == -INFINITY ? 0.f : fast_exp2((ml[i].x - top) * p.scale_log2);
+        l[i] = l[i] * keep + add * ml[i].y;
+        mx[i] = top;
       }
     }
-    if (lane == 0) stat[r] = st;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      const int r = warp + i * kWarps;
+      if (lane == 0 && r < rows) stat[r] = r % p.T < s.draft ? make_float2(mx[i], 1.f / l[i]) : make_float2(0.f, 0.f);
+    }
   }
   __syncthreads();
   float sum[kSlotsEach] = {0.f, 0.f, 0.f, 0.f};
-  for (int r = 0; r < p.rows; ++r) {
+  const float* scores = p.scores + (long long)bh * p.rows * p.score_cap + first;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) {
     const float2 st = stat[r];
-    if (st.y == 0.f) continue;
-    const float* row = p.scores + ((long long)bh * p.rows + r) * p.score_cap + first;
+    float x[kSlotsEach];
 #pragma unroll
     for (int k = 0; k < kSlotsEach; ++k)
-      if (first + k * kThreads < s.len + s.draft)
-        sum[k] += fast_exp2((row[k * kThreads] - st.x) * p.scale_log2) * st.y;
+      x[k] = first + k * kThreads < s.len + s.draft ? scores[(long long)r * p.score_cap + k * kThreads] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kSlotsEach; ++k) {
+      const float e = fast_exp2((x[k] - st.x) * p.scale_log2) * st.y;
+      sum[k] += st.y == 0.f ? 0.f : e;         // a missing token's row: its scores can be anything
+    }
   }
 #pragma unroll
   for (int k = 0; k < kSlotsEach; ++k) {
