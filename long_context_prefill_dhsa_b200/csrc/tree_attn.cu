@@ -55,9 +55,16 @@ constexpr uint32_t kHalfBytes = BM * 128;    // 128 query rows x 64 bf16, 128-by
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
 constexpr uint32_t kKvHalfBytes = BN * 128;
 constexpr uint32_t kKvBytes = 2 * kKvHalfBytes;
-// Caches of up to this many key tiles are not split: a CTA takes whole items
-// and writes O itself, which saves the joining kernel.
-constexpr int kWholeTiles = 8;
+// Items of short caches are not split: a CTA takes whole ones and writes O
+// itself, which saves the joining kernel and, with many items, the draining
+// and refilling of the pipeline. Whole against split, us, 32/8 heads, one token:
+//   500 slots:  1 sequence 10.3 / 10.9, 8 sequences 10.9 / 12.3, 64 sequences 34 / 38
+//   600 slots:  1 sequence 11.0 / 10.9, 8 sequences 11.8 / 13.1, 32 sequences 23 / 26
+//   1000 slots: 1 sequence 14.2 / 10.3, 4 sequences 14.4 / 13.0, 8 sequences 15.0 / 15.8, 32 sequences 30 / 32
+//   2000 slots: 1 sequence 22 / 11, 8 sequences 23 / 21, 64 sequences 94 / 90
+constexpr int kWholeTiles = 5;        // with any number of items
+constexpr int kWholeTilesMany = 8;    // with at least kManyItems, two fifths of the CTAs
+constexpr int kManyItems = 64;
 constexpr float kRaise = 20.f;   // powers of two by which a score may pass its row's reference
 constexpr uint32_t kSmemData = 224 * 1024;   // query tiles (one or two of 32 KB), the rest is the ring of K and V tiles
 constexpr int kMaxStages = (kSmemData - kTileBytes) / kKvBytes;
@@ -578,7 +585,7 @@ Plan make_plan(int B, int Hq, int Hkv, int T, int cap, bool want_weight) {
   q.blocks = ceil_div(q.rows, q.wide * BM);
   q.row_cap = q.rows < BM ? q.rows : BM;
   q.score_cap = ceil_div(cap, BN) * BN;
-  q.whole = cap <= kWholeTiles * BN;
+  q.whole = cap <= (B * (long long)Hkv * q.blocks >= kManyItems ? kWholeTilesMany : kWholeTiles) * BN;
   q.scores = want_weight && q.rows <= kMaxScoreRows;
   const size_t pieces = q.whole ? 0 : (size_t)B * Hkv * q.blocks + kMaxGrid;
   auto round = [](size_t n) { return (n + 255) / 256 * 256; };
