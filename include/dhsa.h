@@ -421,7 +421,8 @@ int dhsa_rotary_qkv(const void* Q, const int64_t* q_strides, const void* K, cons
  *    weight / weight_out  fp32 [B, Hkv, cap], both or neither: for s < lengths[b]
  *             weight_out[s] = weight[s] + sum over the head's Hq/Hkv query
  *             heads and the drafted tokens of p_s; for a drafted token's slot
- *             the sum alone. weight_out may be weight.
+ *             the sum alone. weight_out may be weight. Weights want a
+ *             scale of at least 1e-30.
  *    Rows t >= n_draft[b] of O and lse and the other slots of weight_out are
  *    left as they were. lengths[b] outside [0, cap] and n_draft[b] outside
  *    [0, T] or past the capacity are clamped (DHSA_DEVFLAG_BAD_CACHE); a

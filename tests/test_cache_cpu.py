@@ -59,6 +59,7 @@ TREE = ("Q K ks V vs B Hq Hkv T cap d lengths parents n_draft scale O lse w wo w
     (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(K=FAKE + 2), INV),
     (dict(ks=_strides(1280, 128, 64)), INV), (dict(vs=_strides(1280, 132, 256)), INV), (dict(ws=None), WS),
     (dict(bytes=16), WS), (dict(ws=FAKE + 4), WS), (dict(O=FAKE), INV),
+    (dict(w=FAKE, wo=FAKE, scale=9e-31), INV),
 ])
 def test_tree_refusals(lib, change, want):
     ok = dict(Q=FAKE, K=FAKE, ks=None, V=FAKE, vs=None, B=2, Hq=4, Hkv=2, T=5, cap=50, d=128, lengths=FAKE,

@@ -715,3 +715,29 @@ def test_tree_attn_extreme_scales(lib, scale):
         want = v.mean(0) if scale < 1 else v[s[:, h].argmax()]
         tol = U_BF * (np.abs(v).mean(0) + np.abs(want)) * 1.01 if scale < 1 else 0
         assert np.all(np.abs(_np(out[0, h, 0]) - want) <= tol)
+
+
+@needs_gpu
+@pytest.mark.parametrize("T", [1, 12])          # 4 and 48 rows of a head: scores kept, and computed again
+@pytest.mark.parametrize("scale", [1e-30, 1e30])
+def test_slot_weights_at_extreme_scales(lib, scale, T):
+    """Every slot that a token sees gets the same weight, or the best one all of it.
+
+    Small: the exponent -log2 l, |log2 l| < 9.6, passes through a handful of fp32 operations (log2,
+    a division, three parts, two sums, a product: 8 half steps of it at most, twice that if the tensor
+    core truncates), and log2, exp2 and 1 / l add 2^-22 each: 9.6 ln 2 * 16 U + 3 * 2^-22 < 8e-6."""
+    rng = np.random.default_rng(47)
+    n = 700
+    Q, K, V = _bf(rng, 1, 4, T, D), _bf(rng, 1, 1, n + T, D), _bf(rng, 1, 1, n + T, D)
+    w = torch.zeros(1, 1, n + T, device="cuda")
+    lib.tree_attn(Q, K, V, _i32([n]), softmax_scale=scale, weight=w)
+    s = _np(Q[0]) @ _np(K[0, 0]).T
+    want = np.zeros(n + T)
+    for h in range(4):
+        for t in range(T):
+            if scale < 1:
+                want[: n + t + 1] += 1 / (n + t + 1)
+            else:
+                want[s[h, t, : n + t + 1].argmax()] += 1
+    got = _np(w[0, 0])
+    assert np.all(np.abs(got - want) <= (8e-6 * want if scale < 1 else 0))
