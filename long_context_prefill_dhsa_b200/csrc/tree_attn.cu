@@ -65,7 +65,7 @@ constexpr uint32_t kKvBytes = 2 * kKvHalfBytes;
 constexpr int kWholeTiles = 5;        // with any number of items
 constexpr int kWholeTilesMany = 8;    // with at least kManyItems, two fifths of the CTAs
 constexpr int kManyItems = 64;
-constexpr float kRaise = 20.f;   // powers of two by which a score may pass its row's reference
+constexpr float kRaise = 20.f, kTop = 1048576.f;   // powers of two by which a score may pass its row's reference; its p
 constexpr uint32_t kSmemData = 224 * 1024;   // query tiles (one or two of 32 KB), the rest is the ring of K and V tiles
 constexpr int kMaxStages = (kSmemData - kTileBytes) / kKvBytes;
 
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   Line* line = reinterpret_cast<Line*>(smem + OFF_LINE);
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (warp == W_PRODUCER && lane == 0) {
     *abort_flag = 0;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     tc_fence_before();
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
     tc_fence_after();
-    tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR);
+    tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR), 0);
     share = *line;
   }
   const Waits wait{abort_flag, p.status};
@@ -198,77 +198,88 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
       for (uint32_t q = g > NST ? g - NST : 0; q < g; ++q) mbar_wait(bar(B_FULL + q % NST), (q / NST) & 1, kWaitLimitNs);
     }
   } else if (warp == W_MMA) {
-    // The whole warp runs the loop converged and lane 0 issues.
-    const uint32_t on = lane == 0;
+    // The whole warp runs the loop, and an elected lane issues: operands then
+    // live in uniform registers. (With the loop in one lane, or the lane as
+    // each instruction's predicate, an MMA took 105 to 120 cycles to issue
+    // beside the busy softmax warps, against 65 to execute.)
     const uint32_t idesc_qk = idesc_bf16_f32(MQ, BN, false), idesc_pv = idesc_bf16_f32(MQ, kHeadDim, true);
-    constexpr uint32_t kHi = desc_hi_sw128(1024);
-    const uint32_t q_lo = desc_lo_sw128(sbase, 16), k_lo = desc_lo_sw128(ring, 16);
-    const uint32_t v_lo = desc_lo_sw128(ring, kKvHalfBytes);
+    const uint64_t q_desc = smem_desc_sw128(sbase, 16, 1024), k_desc = smem_desc_sw128(ring, 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(ring, kKvHalfBytes, 1024);
     uint32_t g = 0, n_piece = 0, p_phase = 0;    // p_phase: parity of P's barriers, a bit for each stream
-    auto qk = [&](int s, uint32_t stage) {      // S = Q K^T
-      const uint32_t qa = q_lo + (NQT == 2 ? s * (kQTile >> 4) : 0), ka = k_lo + stage * (kKvBytes >> 4);
+    auto wait_all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+    auto empty = [&](uint32_t q) { return bar(B_EMPTY + q % NST); };
+    auto commit = [&](uint32_t b) {
+      if (elect_one()) mma_commit(b);
+      __syncwarp();
+    };
+    auto qk = [&](int s, uint32_t q, bool done) {      // S = Q K^T; done: the K tile's last use
+      const uint64_t qa = q_desc + (NQT == 2 ? s * (kQTile >> 4) : 0), ka = k_desc + q % NST * (kKvBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ss_lo(on, tmem + s * 128, qa + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4),
-                  ka + (((k >> 2) * kKvHalfBytes + (k & 3) * 32) >> 4), kHi, idesc_qk, k > 0 ? 1u : 0u);
-      mma_commit_on(on, bar(B_SFULL + s));
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tmem + s * 128, qa + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4),
+                 ka + (((k >> 2) * kKvHalfBytes + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+        mma_commit(bar(B_SFULL + s));
+        if (done) mma_commit(empty(q));
+      }
+      __syncwarp();
     };
     auto arrived = [&](uint32_t q) {
-      const bool ok = wait(bar(B_FULL + q % NST), (q / NST) & 1);
+      const bool ok = wait_all(bar(B_FULL + q % NST), (q / NST) & 1);
       tc_fence_after();
       return ok;
     };
-    auto pv = [&](int s, uint32_t q, bool first) {      // O += P V, each half as soon as its P is there
-      const uint32_t va = v_lo + (q % NST) * (kKvBytes >> 4);
+    // O += P V, each half as soon as its P is there; done: the V tile's last use
+    auto pv = [&](int s, uint32_t q, bool first, bool done) {
+      const uint64_t va = v_desc + q % NST * (kKvBytes >> 4);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!wait(bar(B_PREADY + 2 * s + half), (p_phase >> s) & 1)) return false;
-        if (half == 0 && !wait(bar(B_FULL + q % NST), (q / NST) & 1)) return false;
+        if (!wait_all(bar(B_PREADY + 2 * s + half), (p_phase >> s) & 1)) return false;
+        if (half == 0 && !wait_all(bar(B_FULL + q % NST), (q / NST) & 1)) return false;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 4 * half; k < 4 * half + 4; ++k)
-          mma_ts_lo(on, tmem + 256 + s * 128, tmem + s * 128 + k * 8, va + k * (2048 >> 4), kHi, idesc_pv,
-                    (!first || k > 0) ? 1u : 0u);
-        if (half == 0) mma_commit_on(on, bar(B_PVHALF + s));
+          for (int k = 4 * half; k < 4 * half + 4; ++k)
+            mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, va + k * (2048 >> 4), idesc_pv,
+                   (!first || k > 0) ? 1u : 0u);
+          if (half == 0) mma_commit(bar(B_PVHALF + s));
+          else if (done) mma_commit(empty(q));
+        }
+        __syncwarp();
       }
       p_phase ^= 1u << s;
       return true;
     };
     bool ok = true;
     while (ok && walk.next(p, &w)) {
-      if (!wait(bar(B_QREADY), n_piece & 1)) break;
+      const int n = __shfl_sync(0xffffffffu, w.n, 0);
+      if (!wait_all(bar(B_QREADY), n_piece & 1)) break;
       tc_fence_after();
-      for (int i = 0; i < kAhead && i < w.n; ++i) {
+      for (int i = 0; i < kAhead && i < n; ++i) {
         if (!(ok = arrived(g))) break;
-        qk(NQT == 1 ? i : 0, g % NST);
-        if (NQT == 2) qk(1, g % NST);
-        mma_commit_on(on, bar(B_EMPTY + g++ % NST));
+        qk(NQT == 1 ? i : 0, g, NQT == 1);
+        if (NQT == 2) qk(1, g, true);
+        ++g;
       }
-      for (int i = 0; ok && i < w.n; ++i) {
-        const bool more = i + kAhead < w.n;
+      for (int i = 0; ok && i < n; ++i) {
+        const bool more = i + kAhead < n;
         const uint32_t gv = g++, gk = more ? g++ : 0;
-        if (!(ok = pv(NQT == 1 ? i & 1 : 0, gv, i < kAhead))) break;
-        if (NQT == 1) mma_commit_on(on, bar(B_EMPTY + gv % NST));
+        if (!(ok = pv(NQT == 1 ? i & 1 : 0, gv, i < kAhead, NQT == 1))) break;
         if (more) {
           if (!(ok = arrived(gk))) break;
-          qk(NQT == 1 ? i & 1 : 0, gk % NST);
-          if (NQT == 1) mma_commit_on(on, bar(B_EMPTY + gk % NST));
+          qk(NQT == 1 ? i & 1 : 0, gk, NQT == 1);
         }
         if (NQT == 2) {
-          if (!(ok = pv(1, gv, i == 0))) break;
-          mma_commit_on(on, bar(B_EMPTY + gv % NST));
-          if (more) {
-            qk(1, gk % NST);
-            mma_commit_on(on, bar(B_EMPTY + gk % NST));
-          }
+          if (!(ok = pv(1, gv, i == 0, true))) break;
+          if (more) qk(1, gk, true);
         }
       }
       if (!ok) break;
-      mma_commit_on(on, bar(B_OFINAL));
+      commit(bar(B_OFINAL));
       ++n_piece;
     }
     __syncwarp();
-    mma_commit_on(on, bar(B_FINAL));
+    commit(bar(B_FINAL));
     mbar_wait(bar(B_FINAL), 0, kWaitLimitNs);
   } else if (warp >= W_SOFTMAX0) {
     // a stream's warps: HALVES for each lane quarter, 16 lanes each
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     const int cq = lane & 3;
     const uint32_t tS = tmem + ((uint32_t)(quarter * 32 + hf * 16) << 16) + stream * 128;
     const uint32_t tO = tS + 256;
-    const float c = p.scale_log2, raise = fminf(kRaise / c, 3e38f);   // finite, so that -inf + raise is -inf
+    const float c = p.scale_log2;
     const uint64_t c2 = pk2(c, c);
     // written by every softmax warp with the same values
     uint64_t* see = reinterpret_cast<uint64_t*>(smem + OFF_SEE);
@@ -352,10 +363,11 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
             // s[4j + e]: row A, slot k0 + 64 half + 8j + 2cq + e; s[4j + 2 + e]: row B
             uint32_t s[32];
             tmem_ld_16x256b_x8(tSh, s);
-            tmem_wait_ld();
+            tmem_wait_ld_of(s);
             auto S = [&](int gr, int j, int e) -> uint32_t& { return s[4 * j + 2 * gr + e]; };
             const int n0 = w.len - k0 - 64 * half;      // slots of the half that hold cached keys
-            if (n0 < 64) {
+            auto mask = [&] {
+              if (n0 >= 64) return;
 #pragma unroll
               for (int gr = 0; gr < 2; ++gr) {
                 const uint64_t sees = see[(srow0 + rowA + 32 * gr) % p.T];
@@ -367,8 +379,9 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
                   for (int e = 0; e < 2; ++e)
                     if (!((vis >> (8 * j + e)) & 1)) S(gr, j, e) = __float_as_uint(-INFINITY);
               }
-            }
-            if (NQT == 1 && p.scores) {      // for the weight pass
+            };
+            mask();
+            if (HALVES == 1 && p.scores) {      // for the weight pass
 #pragma unroll
               for (int gr = 0; gr < 2; ++gr) {
                 const int r = rowA + 32 * gr;
@@ -378,41 +391,73 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
                 for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(d + 8 * j) = make_uint2(S(gr, j, 0), S(gr, j, 1));
               }
             }
+            // The difference is taken before the scale: scores near the
+            // reference keep their distance to it exactly, however large they
+            // are. A row that has seen nothing yet keeps m = -inf: its p are 0.
+            // pk[2j]: row A, pk[2j + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
+            uint32_t pk[16];
+            uint64_t sum[2];
+            float top = 0.f;
+            auto exps = [&] {
+#pragma unroll
+              for (int gr = 0; gr < 2; ++gr) {
+                sum[gr] = 0ull;
+                if (groups > gr) {
+                  const float n = m[gr] == -INFINITY ? 0.f : -m[gr];
+                  const uint64_t n2 = pk2(n, n);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    float x0, x1;
+                    unpk2(mul2(add2(pk2(__uint_as_float(S(gr, j, 0)), __uint_as_float(S(gr, j, 1))), n2), c2), x0, x1);
+                    x0 = fast_exp2(x0);
+                    x1 = fast_exp2(x1);
+                    top = max3(top, x0, x1);
+                    sum[gr] = add2(sum[gr], pk2(x0, x1));
+                    pk[2 * j + gr] = pack_bf16x2(x0, x1);
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) pk[2 * j + gr] = 0u;
+                }
+              }
+            };
+            // The first half has no reference yet. (With two query tiles the
+            // branch costs the loop its registers: 157 us against 144 for 256
+            // rows over 131000 slots; with one it saves 0.3 of 7.7 for 37.)
+            const bool start = NQT == 1 && i < step && half == 0;
+            if (!start) exps();
             // Scores are taken relative to a reference of the row, its
             // largest score when the reference was last set: it is set again,
             // and O rescaled, only when a score passes it by 2^kRaise. P and
             // the sums have fp32's exponent range, so O / l is the same; the
-            // test needs no exchange between the row's threads.
-            float x[2];
-            bool up = false;
-#pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-              x[gr] = -INFINITY;
-              if (groups <= gr) continue;
-              auto F = [&](int j, int e) { return __uint_as_float(S(gr, j, e)); };
-              float a0 = fmaxf(F(0, 0), F(0, 1)), a1 = fmaxf(F(1, 0), F(1, 1));
-#pragma unroll
-              for (int j = 2; j < 8; j += 2) {
-                a0 = max3(a0, F(j, 0), F(j, 1));
-                a1 = max3(a1, F(j + 1, 0), F(j + 1, 1));
+            // test needs no exchange between the row's threads, and comes
+            // after the exponentials, which are seldom done again.
+            const bool unset = m[0] == -INFINITY || (groups > 1 && m[1] == -INFINITY);
+            if (start || __any_sync(0xffffffffu, top > kTop || unset)) {
+              if (!start) {      // the scores again, in place of their p
+                tmem_ld_16x256b_x8(tSh, s);
+                tmem_wait_ld_of(s);
+                mask();
               }
-              x[gr] = fmaxf(a0, a1);
-              up = up || x[gr] > m[gr] + raise;
-            }
-            if (__any_sync(0xffffffffu, up)) {
               float f[2];
 #pragma unroll
               for (int gr = 0; gr < 2; ++gr) {
-                x[gr] = fmaxf(x[gr], __shfl_xor_sync(0xffffffffu, x[gr], 1));
-                x[gr] = fmaxf(x[gr], __shfl_xor_sync(0xffffffffu, x[gr], 2));
-                const bool r = x[gr] > m[gr] + raise;
-                f[gr] = r ? fast_exp2((m[gr] - x[gr]) * c) : 1.f;
-                if (r) m[gr] = x[gr];
+                float x = -INFINITY;
+                if (groups > gr) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) x = max3(x, __uint_as_float(S(gr, j, 0)), __uint_as_float(S(gr, j, 1)));
+                }
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                const bool r = (x - m[gr]) * c > kRaise;      // the row's own need: no other row shows in it
+                f[gr] = r ? fast_exp2((m[gr] - x) * c) : 1.f;
+                if (r) m[gr] = x;
                 l[gr] = mul2(l[gr], pk2(f[gr], f[gr]));
               }
               // S complete implies the products of the stream's earlier tiles complete
               if (half == 1 && !(ok = wait(bar(B_PVHALF + stream), n_t & 1))) break;
               tc_fence_after();
+              exps();
               if (i >= step || half == 1) {
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
@@ -423,33 +468,10 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
                   for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
                   tmem_st_16x256b_x4(tO + 32 * q, o);
                 }
-                tmem_wait_st();
               }
             }
-            // The difference is taken before the scale: scores near the
-            // reference keep their distance to it exactly, however large they
-            // are. A row that has seen nothing yet keeps m = -inf: its p are 0.
-            // pk[2j]: row A, pk[2j + 1]: row B (16x128b: lanes t / 4 and t / 4 + 8)
-            uint32_t pk[16];
 #pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-              if (groups > gr) {
-                const float n = m[gr] == -INFINITY ? 0.f : -m[gr];
-                const uint64_t n2 = pk2(n, n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  float x0, x1;
-                  unpk2(mul2(add2(pk2(__uint_as_float(S(gr, j, 0)), __uint_as_float(S(gr, j, 1))), n2), c2), x0, x1);
-                  x0 = fast_exp2(x0);
-                  x1 = fast_exp2(x1);
-                  l[gr] = add2(l[gr], pk2(x0, x1));
-                  pk[2 * j + gr] = pack_bf16x2(x0, x1);
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) pk[2 * j + gr] = 0u;
-              }
-            }
+            for (int gr = 0; gr < 2; ++gr) l[gr] = add2(l[gr], sum[gr]);
             tmem_st_16x128b_x8(tP, pk);
             tmem_wait_st();
           }

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   uint64_t* see = reinterpret_cast<uint64_t*>(smem + OFF_SEE);
   float* xsum = reinterpret_cast<float*>(smem + OFF_XSUM);
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR), 0);
   const Waits wait{abort_flag, p.status};
   Pieces walk{line->start, line->end, line->base, line->b};
   Piece w{};
@@ -152,47 +152,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
         mbar_wait(bar(W_FULL + q % kStages), (q / kStages) & 1, kWaitLimitNs);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t g = 0, used[2] = {0, 0}, n_q = 0;
-      bool ok = true;
-      while (ok && walk.next(p, &w)) {
-        for (int rb = 0; ok && rb < walks; ++rb) {
-          if (!(ok = wait(bar(W_QREADY), n_q++ & 1))) break;
-          const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock);
-          // each half of the columns on its own: its warps free it on their own
-          const int n_half = ((n_rows + 31) & ~31) / 2;
-          const uint32_t idesc = idesc_bf16_f32(BN, n_half, false);
-          for (int i = 0; ok && i < w.n; ++i, ++g) {
-            const int s = i & 1;
-            const uint32_t st = g % kStages;
-            if (!(ok = wait(bar(W_FULL + st), (g / kStages) & 1))) break;
-            const uint32_t ka = sbase + OFF_RING + st * kTileBytes;
-            for (int half = 0; half < 2; ++half) {
-              if (used[s] > 0 && !(ok = wait(bar(W_SEMPTY + 2 * s + half), (used[s] - 1) & 1))) break;
-              tc_fence_after();
-              const uint32_t d = tmem + s * 256 + half * n_half, qa = sbase + OFF_Q + half * n_half * 128;
+    // the whole warp runs the loop and an elected lane issues, as in tree_attn.cu
+    auto wait_all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+    uint32_t g = 0, used[2] = {0, 0}, n_q = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &w)) {
+      const int n = __shfl_sync(0xffffffffu, w.n, 0);
+      for (int rb = 0; ok && rb < walks; ++rb) {
+        if (!(ok = wait_all(bar(W_QREADY), n_q++ & 1))) break;
+        const int n_rows = min(p.rows - rb * kRowBlock, kRowBlock);
+        // each half of the columns on its own: its warps free it on their own
+        const int n_half = ((n_rows + 31) & ~31) / 2;
+        const uint32_t idesc = idesc_bf16_f32(BN, n_half, false);
+        for (int i = 0; ok && i < n; ++i, ++g) {
+          const int s = i & 1;
+          const uint32_t st = g % kStages;
+          if (!(ok = wait_all(bar(W_FULL + st), (g / kStages) & 1))) break;
+          const uint64_t ka = smem_desc_sw128(sbase + OFF_RING + st * kTileBytes, 16, 1024);
+          for (int half = 0; half < 2; ++half) {
+            if (used[s] > 0 && !(ok = wait_all(bar(W_SEMPTY + 2 * s + half), (used[s] - 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + s * 256 + half * n_half;
+            const uint64_t qa = smem_desc_sw128(sbase + OFF_Q + half * n_half * 128, 16, 1024);
+            const uint64_t ones = smem_desc_noswz(sbase + OFF_ONES, 128, 256);
+            const uint64_t bias = smem_desc_noswz(sbase + OFF_BIAS + half * n_half * 32, 128, 256);
+            if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t c = (k & 3) * 32;
-                mma_ss(d, smem_desc_sw128(ka + (k >> 2) * kHalfBytes + c, 16, 1024),
-                       smem_desc_sw128(qa + (k >> 2) * kQHalfBytes + c, 16, 1024), idesc, k > 0 ? 1u : 0u);
-              }
+              for (int k = 0; k < 8; ++k)
+                mma_ss(d, ka + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+                       qa + (((k >> 2) * kQHalfBytes + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
               // S - M first, as an exact difference of like numbers, then - log l
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_ss(d, smem_desc_noswz(sbase + OFF_ONES, 128, 256),
-                       smem_desc_noswz(sbase + OFF_BIAS + k * kRowBlock * 32 + half * n_half * 32, 128, 256), idesc, 1u);
+              for (int k = 0; k < 2; ++k) mma_ss(d, ones, bias + (k * kRowBlock * 32 >> 4), idesc, 1u);
               mma_commit(bar(W_SFULL + 2 * s + half));
+              if (half == 1) mma_commit(bar(W_EMPTY + st));
             }
-            if (!ok) break;
-            ++used[s];
-            mma_commit(bar(W_EMPTY + st));
+            __syncwarp();
           }
+          if (!ok) break;
+          ++used[s];
         }
       }
-      mma_commit(bar(W_FINAL));
-      mbar_wait(bar(W_FINAL), 0, kWaitLimitNs);
     }
+    if (elect_one()) mma_commit(bar(W_FINAL));
+    mbar_wait(bar(W_FINAL), 0, kWaitLimitNs);
   } else if (warp >= 4) {
     // per S^T buffer two groups of four warps, one for each half of the columns
     const int buf = ((warp - 4) >> 2) & 1, upper = (warp - 4) >> 3, quarter = warp & 3, key = quarter * 32 + lane;
