@@ -21,6 +21,8 @@
 // of counts and their barriers.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace cg = cooperative_groups;
@@ -139,7 +141,16 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
   const bool all = m == n_cand;            // every candidate stays: no ranking
   uint32_t cut = 0;                        // the m-th largest key
   uint32_t ties = 0;                       // how many of the slots with that key stay
-  auto key_of = [&](int s) { return s - blk0 < p.keys_held ? keys[s - blk0] : key_from(s, w_in[s], pos_in[s]); };
+  // a block whose slots all have their key in shared memory has loops of its own
+  const bool held = per_warp * kEvWarps <= p.keys_held;
+  auto key_of = [&](auto in_shared, int s) -> uint32_t {
+    if constexpr (in_shared.value) return keys[s - blk0];
+    return s - blk0 < p.keys_held ? keys[s - blk0] : key_from(s, w_in[s], pos_in[s]);
+  };
+  auto with_keys = [&](auto f) {
+    if (held) f(std::true_type{});
+    else f(std::false_type{});
+  };
   if (!all) {
     for (int i = tid; i < kRounds * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
@@ -168,13 +179,14 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
 #pragma unroll 1
     for (int r = 0; r < kRounds; ++r) {
       const int shift = 24 - 8 * r;
-      if (r > 0) {
+      if (r > 0)
+        with_keys([&](auto in_shared) {
 #pragma unroll 4
-        for (int s = w0 + lane; s < w1; s += 32) {       // the lane's own keys
-          const uint32_t k = key_of(s);
-          if ((k ^ cut) >> (shift + 8) == 0) atomicAdd(&sh.hist[r][(k >> shift) & 255u], 1u);
-        }
-      }
+          for (int s = w0 + lane; s < w1; s += 32) {       // the lane's own keys
+            const uint32_t k = key_of(in_shared, s);
+            if ((k ^ cut) >> (shift + 8) == 0) atomicAdd(&sh.hist[r][(k >> shift) & 255u], 1u);
+          }
+        });
       cluster.sync();
       // the cluster's histogram: kParts threads per bin add up every kParts-th block's
       {
@@ -221,14 +233,23 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
 
   // counts of the warp's slots, then of every range before them
   Counts mine{0, 0, 0, 0};
-#pragma unroll 4
-  for (int s = w0 + lane; s < w1; s += 32) {
-    const uint32_t k = all ? (is_cand(s) ? 1u : 0u) : key_of(s);
-    const bool low = s < m, gt = k > cut, eq = !all && k == cut;
+  auto count = [&](int s, bool gt, bool eq) {
+    const bool low = s < m;
     mine.gt_low += gt && low;
     mine.gt_high += gt && !low;
     mine.eq_low += eq && low;
     mine.eq_high += eq && !low;
+  };
+  if (all) {
+    for (int s = w0 + lane; s < w1; s += 32) count(s, is_cand(s), false);
+  } else {
+    with_keys([&](auto in_shared) {
+#pragma unroll 4
+      for (int s = w0 + lane; s < w1; s += 32) {
+        const uint32_t k = key_of(in_shared, s);
+        count(s, k > cut, k == cut);
+      }
+    });
   }
   mine.gt_low = __reduce_add_sync(0xffffffffu, mine.gt_low);
   mine.gt_high = __reduce_add_sync(0xffffffffu, mine.gt_high);
@@ -260,30 +281,30 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
   uint32_t src_at = first(bk.high, rank) + first(wk.high, warp);
 
   const uint32_t lt = (1u << lane) - 1;
-  // whether slot s stays; called for 32 consecutive slots by a whole warp, in
-  // order, with the running count of equal keys before them
-  auto stays = [&](int s) {
-    if (all) return s < w1 && is_cand(s);
-    const uint32_t k = s < w1 ? key_of(s) : 0u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, s < w1 && k == cut);
-    const bool yes = s < w1 && (k > cut || (k == cut && tie_run + __popc(eq & lt) < ties));
-    tie_run += __popc(eq);
-    return yes;
-  };
-
-  // the lists
+  // the lists: for 32 consecutive slots of the warp at a time, in order
   int32_t* hole_list = p.lists + row;
   int32_t* src_list = hole_list + p.cap / 2;   // min(m, n_all - m) <= cap / 2 rows move
-#pragma unroll 2
-  for (int s0 = w0; s0 < w1; s0 += 32) {
-    const int s = s0 + lane;
-    const bool yes = stays(s);
+  auto list = [&](int s, bool yes) {
     const bool hole = s < m && s < w1 && !yes, src = s >= m && yes;
     const uint32_t hb = __ballot_sync(0xffffffffu, hole), sb = __ballot_sync(0xffffffffu, src);
     if (hole) hole_list[hole_at + __popc(hb & lt)] = s;
     if (src) src_list[src_at + __popc(sb & lt)] = s;
     hole_at += __popc(hb);
     src_at += __popc(sb);
+  };
+  if (all) {
+    for (int s0 = w0; s0 < w1; s0 += 32) list(s0 + lane, s0 + lane < w1 && is_cand(s0 + lane));
+  } else {
+    with_keys([&](auto in_shared) {
+#pragma unroll 4
+      for (int s0 = w0; s0 < w1; s0 += 32) {
+        const int s = s0 + lane;
+        const uint32_t k = s < w1 ? key_of(in_shared, s) : 0u;
+        const uint32_t eq = __ballot_sync(0xffffffffu, s < w1 && k == cut);
+        list(s, s < w1 && (k > cut || (k == cut && tie_run + __popc(eq & lt) < ties)));
+        tie_run += __popc(eq);
+      }
+    });
   }
   if (all && (copy_w || copy_pos || idx_row)) {
     for (int s0 = rank * kEvThreads + tid; s0 < m; s0 += C * kEvThreads * kBatch) {
