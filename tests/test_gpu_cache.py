@@ -741,3 +741,97 @@ def test_slot_weights_at_extreme_scales(lib, scale, T):
                 want[s[h, t, : n + t + 1].argmax()] += 1
     got = _np(w[0, 0])
     assert np.all(np.abs(got - want) <= (8e-6 * want if scale < 1 else 0))
+
+
+def _three_calls(lib, rng):
+    """Arguments of the three calls with every optional one, caches as views of slot-major storage."""
+    B, Hq, Hkv, T, cap = 2, 4, 2, 3, 40
+    cache = lambda: _bf(rng, B, cap, Hkv, D).transpose(1, 2)
+    f = torch.from_numpy(10000.0 ** (-np.arange(64) / 64)).cuda()
+    n, t = _i32([20, 31]), _i32([3, 2])
+    wt = lambda: torch.from_numpy(rng.random((B, Hkv, cap)).astype(np.float32)).cuda()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    return {
+        "rotary_qkv": dict(Q=_bf(rng, B, T, Hq, D).transpose(1, 2), K=_bf(rng, B, T, Hkv, D).transpose(1, 2), inv_freq=f,
+                           V=_bf(rng, B, Hkv, T, D), start=n.clone(), n_new=t, slots=n, Q_out=torch.zeros_like(_bf(rng, B, Hq, T, D)),
+                           K_out=cache(), V_out=cache(), pos_out=i32(B, Hkv, cap), factor=1, interleaved=True),
+        "tree_attn": dict(Q=_bf(rng, B, Hq, T, D), K=cache(), V=cache(), lengths=n, parents=_i32([[-1, 0, 0], [-1, 0, 1]]),
+                          n_draft=t, softmax_scale=0.25, weight=wt(), weight_out=wt(), out=_bf(rng, B, Hq, T, D),
+                          lse=torch.zeros(B, Hq, T, device="cuda")),
+        "cache_evict": dict(K=cache(), V=cache(), weight=wt(), pos=i32(B, Hkv, cap), lengths=n, keep=12, next_pos=n + 3,
+                            n_draft=t, accept=torch.tensor([5, 1], device="cuda"), sinks=0, recent=4, weight_out=wt(),
+                            pos_out=i32(B, Hkv, cap), lengths_out=i32(B), index=i32(B, Hkv, 12)),
+    }
+
+
+class _TakesNothing:
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+@needs_gpu
+@pytest.mark.parametrize("name", ["rotary_qkv", "tree_attn", "cache_evict"])
+@pytest.mark.parametrize("optional", [True, False])
+def test_calls_with_their_checks_in_python(lib, monkeypatch, name, optional):
+    """The compiled checks take an ordinary call, and make the same one as the checks in Python."""
+    results = []
+    for python in (False, True):
+        a = _three_calls(lib, np.random.default_rng(51))[name]
+        if not optional:
+            for k in ("Q_out", "K_out", "V_out", "pos_out", "slots", "n_new", "out", "lse", "weight_out", "lengths_out",
+                      "index", "softmax_scale"):
+                a.pop(k, None)
+        if name == "tree_attn" and not optional:
+            a["n_draft"], a["parents"] = None, None     # rows of missing tokens of a new `out` hold anything
+        lib._load_marshal()
+        with monkeypatch.context() as m:
+            if python:
+                m.setattr(lib, "_marshal", _TakesNothing())
+            else:
+                real, taken = lib._marshal, []
+
+                class Watch:
+                    def __getattr__(self, n):
+                        def call(*x):
+                            taken.append(getattr(real, n)(*x))
+                            return taken[-1]
+                        return call
+                m.setattr(lib, "_marshal", Watch())
+            r = getattr(lib, name)(**a)
+            assert python or (len(taken) == 1 and taken[0] is not None and type(taken[0]) is not int)
+        tensors = [x for x in a.values() if isinstance(x, torch.Tensor)]
+        results.append(tensors + list(r if isinstance(r, tuple) else (r,)))
+        if name == "rotary_qkv" and optional:
+            assert r[0] is a["Q_out"] and r[1] is a["K_out"] and r[2] is a["V_out"]
+        elif optional:
+            assert r is (a["out"] if name == "tree_attn" else a["lengths_out"])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
+@needs_gpu
+@pytest.mark.parametrize("name", ["rotary_qkv", "tree_attn", "cache_evict"])
+def test_every_tensor_is_checked(lib, name):
+    """Each tensor of each call with another type, shape, layout or place is refused, before anything runs."""
+    good = _three_calls(lib, np.random.default_rng(52))[name]
+    rows = {"Q", "K", "V", "K_out", "V_out"} - ({"Q"} if name == "tree_attn" else set())
+    for key, t in good.items():
+        if not isinstance(t, torch.Tensor):
+            continue
+        other = torch.float64 if t.dtype != torch.float64 else torch.float32
+        bad = [t.to(other), torch.cat([t, t], -1), t.cpu(), t.tolist()]
+        wide = torch.zeros(*t.shape, 2, dtype=t.dtype, device="cuda")[..., 0]        # elements two apart
+        if t.dim() > 1 or t.numel() > 1:
+            bad.append(wide)
+        if key not in rows and t.dim() > 1:
+            bad.append(torch.zeros(*t.shape[1:], t.shape[0], dtype=t.dtype, device="cuda").movedim(-1, 0))
+        for b in bad:
+            if key == "inv_freq" and b is bad[1]:
+                b = torch.cat([t, t])                # 256 rotated elements of 128
+            with pytest.raises((TypeError, ValueError, lib.DHSAError)):
+                getattr(lib, name)(**{**good, key: b})
+    for key in {"rotary_qkv": ["inv_freq"], "tree_attn": ["Q", "K", "V", "lengths"],
+                "cache_evict": ["K", "V", "weight", "pos", "lengths"]}[name]:
+        with pytest.raises((TypeError, ValueError, AttributeError, lib.DHSAError)):
+            getattr(lib, name)(**{**good, key: None})
+    torch.cuda.synchronize()
