@@ -69,7 +69,8 @@ __device__ __forceinline__ int line_len(const TreeParams& p, int b) {
 // With fewer items than CTAs each item gets a whole number of CTAs in
 // proportion to its tiles (`each` of them in sequence b, the first being CTA
 // `first`), so that no CTA has parts of two: such a CTA would drain one item
-// and fill its pipeline again for the next, about as long as five tiles. With
+// and fill its pipeline again for the next, about as long as five tiles (trees
+// of 32 over 8 items of 8K slots: 48 us by items, 58 in equal shares). With
 // more items the line is cut into equal shares.
 // (At most 2^31 cached slots and 32 query blocks: the line is shorter than 2^30.)
 struct Line {

@@ -4,7 +4,9 @@
 // Both are a pass over data that mostly sits in L2, and short: what counts is
 // the chain of dependent loads. So every row, and every block of slots, finds
 // its row statistics for itself from the pieces (at most one per CTA), and
-// where both are wanted they are one launch.
+// where both are wanted they are one launch. Measured: 32 rows of 18 pieces
+// each 3 us behind the attention, 2048 rows 5 us (19 MB of pieces); 256 rows of
+// 32 sequences with the weights of 1.2M slots 8 us.
 #include "tree.cuh"
 
 namespace dhsa {

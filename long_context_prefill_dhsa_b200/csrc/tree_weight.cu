@@ -10,7 +10,8 @@
 // TMEM, so the epilogue reads nothing but its column. (Read from shared memory
 // per pair of rows instead, they took a quarter of the kernel's time.) K is read once more (256
 // bytes per slot); up to about 180 rows that read is the bound, above them
-// the exponentials (16 per cycle and SM).
+// the exponentials (16 per cycle and SM). Measured: 256 rows of 8 heads over
+// 131008 slots 93 us, 2.9e12 exponentials a second, 64% of what the units can do.
 //
 // Warp 0 streams the K tiles, warp 1 issues the MMAs into two S^T buffers of
 // 256 columns; eight warps take the even and eight the odd tiles, four for each
