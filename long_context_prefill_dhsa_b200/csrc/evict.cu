@@ -40,7 +40,12 @@ constexpr int kRounds = 4;
 constexpr int kMaxCluster = 16;           // above 8 the launch asks for the non-portable size
 constexpr int kLargeClusters = 14;        // clusters of 16 that the GPU runs at a time
 constexpr int kBatch = 4;                 // slots whose weight and position a thread loads at a time
-constexpr int kKeysPerBlock = 48 * 1024;  // keys held in shared memory; later ones are derived again
+// Keys held in shared memory. A block with more slots than that derives keys
+// again from the weights, and takes as long whether it holds 26K or 48K of them
+// (4 heads of 1M slots: 205 us); with 26K two blocks fit an SM, and the clusters
+// of 8 heads run at one time: 269 us against 419.
+constexpr int kKeysPerBlock = 48 * 1024;
+constexpr int kKeysOfMore = 26 * 1024;
 constexpr int kSlotsPerBlock = 8192;      // slots a block of a cluster is given before another one joins
 
 struct EvictParams {
@@ -414,7 +419,7 @@ int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, c
   p.status = status;
   const int C = cluster_size(cap, B * Hkv);
   const int span = ceil_div(cap, C * kEvThreads) * kEvThreads;   // slots of one block at most
-  p.keys_held = span < kKeysPerBlock ? span : kKeysPerBlock;
+  p.keys_held = span <= kKeysPerBlock ? span : kKeysOfMore;
   const size_t smem = sizeof(EvictShared) + 4u * (size_t)p.keys_held;
   static bool done[64] = {false};
   int dev = 0, sms = 0;

@@ -835,3 +835,14 @@ def test_every_tensor_is_checked(lib, name):
         with pytest.raises((TypeError, ValueError, AttributeError, lib.DHSAError)):
             getattr(lib, name)(**{**good, key: None})
     torch.cuda.synchronize()
+
+
+@needs_gpu
+@pytest.mark.parametrize("case", [
+    (1, 1, 800_000, [799_990], 100_000, {"n_draft": [10], "accept": [0b1100110011], "sinks": 4, "recent": 64}),
+    (2, 1, 790_000, [790_000, 17], 700_001, {"in_place": True, "with_index": False}),    # 49K slots a block
+    (3, 5, 131_072, [131_072, 131_000, 70_000], 5000, {"recent": 32}),     # more heads than clusters of 16 at a time
+], ids=["1x800k", "2x790k", "15x128k"])
+def test_evict_blocks_with_more_slots_than_keys_and_many_heads(lib, case):
+    B, Hkv, cap, lengths, keep, opt = case
+    _check_evict(lib, np.random.default_rng(cap), B, Hkv, cap, lengths, keep, **opt)
