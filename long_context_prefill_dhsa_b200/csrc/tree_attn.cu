@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     uint32_t g = 0, n_t = 0, n_piece = 0;   // ring tiles and this stream's tiles used so far, pieces
     bool ok = true;
     while (ok && walk.next(p, &w)) {
-      // ---- the query tiles: each warp loads an equal share of the shared-memory rows
+      // ---- the query tiles: each warp loads an equal share of the shared-memory rows; rows of
+      // missing tokens are zeros (NaN among them would never get a reference)
       const __nv_bfloat16* q_head = p.Q + ((long long)w.b * p.Hq + (long long)w.h * p.G) * p.T * kHeadDim;
       const int row0 = w.block * (NQT == 2 ? 2 * BM : BM);      // first row of the block
       const int ch = lane & 15;
@@ -309,7 +310,8 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
         const int at = (warp - W_SOFTMAX0) * 2 * kEach + it * 2 + (lane >> 4), L = at & (MQ - 1);
         const int r = row0 + (at >> kQBits) * BM + 4 * (L & (kLanes - 1)) + (L >> (kQBits - 2));
         v[it] = make_uint4(0, 0, 0, 0);
-        if (r < p.rows) v[it] = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
+        if (r < p.rows && (w.draft == p.T || r % p.T < w.draft))
+          v[it] = *reinterpret_cast<const uint4*>(q_head + (long long)r * kHeadDim + ch * 8);
       }
 #pragma unroll
       for (int it = 0; it < kEach; ++it) {
