@@ -426,10 +426,11 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
                 }
               }
             };
-            // The first half has no reference yet. (With two query tiles the
-            // branch costs the loop its registers: 157 us against 144 for 256
-            // rows over 131000 slots; with one it saves 0.3 of 7.7 for 37.)
-            const bool start = NQT == 1 && i < step && half == 0;
+            // The first half has no reference yet. (With 640 threads the branch
+            // costs the loop its registers: 157 us against 144 for 256 rows
+            // over 131000 slots, 17.8 against 16.6 for 128 rows of 8 sequences
+            // over 500; with 384 it saves 0.3 of 7.7 us for 37 slots.)
+            const bool start = HALVES == 1 && i < step && half == 0;
             if (!start) exps();
             // Scores are taken relative to a reference of the row, its
             // largest score when the reference was last set: it is set again,
