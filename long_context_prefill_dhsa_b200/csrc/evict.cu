@@ -16,16 +16,17 @@
 // One thread-block cluster per (sequence, head): its blocks split the slots,
 // hold the keys in shared memory, and read each other's histograms and
 // counts through distributed shared memory, so the whole update is one
-// launch. Bound: 8 bytes (weight, position) per slot and 1 KB per moved row
+// launch (two when few heads have many rows to move). Bound: 8 bytes (weight, position) per slot and 1 KB per moved row
 // against HBM; for small caches the chain of four histogram rounds, one round
-// of counts and their barriers. Measured: 8 heads of 131072 slots to 8192, 43.6
+// of counts and their barriers. Measured: 8 heads of 131072 slots to 8192, 42.5
 // us, 27 of them ranking (about 6 us until the keys are there, 3 a round, 10
-// for counts and lists) and 13 moving 61K rows (63 MB at 5 TB/s).
+// for counts and lists) and 12 moving 61K rows (63 MB at 5.3 TB/s).
 #include <cooperative_groups.h>
 
 #include <type_traits>
 
 #include "cache.cuh"
+#include "sm100_ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -37,6 +38,7 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kBins = 256;
 constexpr int kParts = kEvThreads / kBins;
 constexpr int kRounds = 4;
+constexpr int kSplitMoves = 256;           // moves per block from which a second kernel does them
 constexpr int kMaxCluster = 16;           // above 8 the launch asks for the non-portable size
 constexpr int kLargeClusters = 14;        // clusters of 16 that the GPU runs at a time
 constexpr int kBatch = 4;                 // slots whose weight and position a thread loads at a time
@@ -58,6 +60,7 @@ struct EvictParams {
   float* weight_out;
   int32_t *pos_out, *lengths_out, *index;
   int32_t* lists;          // [B * Hkv][cap]: holes in the first half, their sources in the second
+  uint32_t* moves;         // [B * Hkv] rows that move, when a second kernel moves them (else null)
   int B, Hkv, cap, keep, sinks, recent, index_cols, max_draft, keys_held;
   unsigned int* status;
 };
@@ -102,6 +105,51 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {     // inc
   return v;
 }
 
+// The moves first, first + stride, ... of a head, by one warp: 16 lanes carry
+// a slot's K row, 16 its V row. Sources and destinations are apart, so the
+// moves need no order.
+__device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, int bh, int lane, uint32_t moves,
+                                          uint32_t first, uint32_t stride) {
+  const long long row = (long long)bh * p.cap;
+  const float* w_in = p.weight + row;
+  const int32_t* pos_in = p.pos + row;
+  float* w_out = p.weight_out + row;
+  int32_t* pos_out = p.pos_out + row;
+  int32_t* idx_row = p.index ? p.index + (long long)bh * p.index_cols : nullptr;
+  const int32_t *hole_list = p.lists + row, *src_list = hole_list + p.cap / 2;
+  const bool is_v = lane >= 16;
+  __nv_bfloat16* base = is_v ? p.V + b * p.vs.b + h * p.vs.h : p.K + b * p.ks.b + h * p.ks.h;
+  const long long rs = is_v ? p.vs.r : p.ks.r;
+  base += (lane & 15) * 8;
+  constexpr int kInFlight = 4;
+  // lane l of a warp holds the l-th of its next 32 moves
+  for (uint32_t r0 = first; r0 < moves; r0 += 32 * stride) {
+    const uint32_t at = r0 + lane * stride;
+    const int my_dst = at < moves ? hole_list[at] : -1, my_from = at < moves ? src_list[at] : 0;
+    if (my_dst >= 0) {
+      w_out[my_dst] = w_in[my_from];
+      pos_out[my_dst] = pos_in[my_from];
+      if (idx_row) idx_row[my_dst] = my_from;
+    }
+    const int n = __popc(__ballot_sync(0xffffffffu, my_dst >= 0));
+    for (int k0 = 0; k0 < n; k0 += kInFlight) {
+      uint4 x[kInFlight];
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        const int from = __shfl_sync(0xffffffffu, my_from, (k0 + k) & 31);
+        if (k0 + k < n) x[k] = *reinterpret_cast<const uint4*>(base + from * rs);
+      }
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        const int dst = __shfl_sync(0xffffffffu, my_dst, (k0 + k) & 31);
+        if (k0 + k < n) *reinterpret_cast<uint4*>(base + dst * rs) = x[k];
+      }
+    }
+  }
+}
+
+// SPLIT: the rows are moved by the next kernel
+template <bool SPLIT>
 __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams p) {
   extern __shared__ __align__(16) unsigned char ev_smem[];
   EvictShared& sh = *reinterpret_cast<EvictShared*>(ev_smem);
@@ -338,37 +386,19 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const EvictParams 
   // the cluster's lists are complete, and nobody reads a weight or position
   // to rank it any more
   cluster.sync();
-  // one warp per moved slot: 16 lanes carry its K row, 16 its V row
-  const bool is_v = lane >= 16;
-  __nv_bfloat16* base = is_v ? p.V + b * p.vs.b + h * p.vs.h : p.K + b * p.ks.b + h * p.ks.h;
-  const long long rs = is_v ? p.vs.r : p.ks.r;
-  base += (lane & 15) * 8;
-  constexpr int kInFlight = 4;
-  const uint32_t stride = C * kEvWarps;
-  // lane l of a warp holds the l-th of its next 32 moves
-  for (uint32_t r0 = rank * kEvWarps + warp; r0 < moves; r0 += 32 * stride) {
-    const uint32_t at = r0 + lane * stride;
-    const int my_dst = at < moves ? hole_list[at] : -1, my_from = at < moves ? src_list[at] : 0;
-    if (my_dst >= 0) {
-      w_out[my_dst] = w_in[my_from];
-      pos_out[my_dst] = pos_in[my_from];
-      if (idx_row) idx_row[my_dst] = my_from;
-    }
-    const int n = __popc(__ballot_sync(0xffffffffu, my_dst >= 0));
-    for (int k0 = 0; k0 < n; k0 += kInFlight) {
-      uint4 x[kInFlight];
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        const int from = __shfl_sync(0xffffffffu, my_from, (k0 + k) & 31);
-        if (k0 + k < n) x[k] = *reinterpret_cast<const uint4*>(base + from * rs);
-      }
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        const int dst = __shfl_sync(0xffffffffu, my_dst, (k0 + k) & 31);
-        if (k0 + k < n) *reinterpret_cast<uint4*>(base + dst * rs) = x[k];
-      }
-    }
+  if (SPLIT) {
+    if (rank == 0 && tid == 0) p.moves[bh] = moves;
+  } else {
+    move_rows(p, b, h, bh, lane, moves, rank * kEvWarps + warp, C * kEvWarps);
   }
+}
+
+// The rows of few heads, moved by the whole GPU.
+__global__ void __launch_bounds__(kEvThreads, 2) evict_move_kernel(const EvictParams p, int blocks) {
+  const int bh = blockIdx.x / blocks, part = blockIdx.x % blocks;
+  ptx::wait_for_predecessors();
+  move_rows(p, bh / p.Hkv, bh % p.Hkv, bh, threadIdx.x & 31, p.moves[bh], part * kEvWarps + (threadIdx.x >> 5),
+            blocks * kEvWarps);
 }
 
 // More blocks per head shorten the loops over its slots and lengthen the
@@ -384,7 +414,8 @@ int cluster_size(int cap, int heads) {
 
 }  // namespace
 
-size_t evict_ws_bytes(int B, int Hkv, int cap) { return sizeof(int32_t) * (size_t)B * Hkv * cap; }
+// the lists, and each head's number of moves
+size_t evict_ws_bytes(int B, int Hkv, int cap) { return sizeof(int32_t) * (size_t)B * Hkv * ((size_t)cap + 1); }
 int evict_max_drafts() { return 64; }
 
 int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, const float* weight,
@@ -421,12 +452,22 @@ int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, c
   const int span = ceil_div(cap, C * kEvThreads) * kEvThreads;   // slots of one block at most
   p.keys_held = span <= kKeysPerBlock ? span : kKeysOfMore;
   const size_t smem = sizeof(EvictShared) + 4u * (size_t)p.keys_held;
-  static bool done[64] = {false};
+  static bool done[2][64] = {{false}};
   int dev = 0, sms = 0;
   cudaError_t e = this_device(&dev, &sms);
-  if (e == cudaSuccess && !done[dev])
-    e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) e = allow_smem(evict_kernel, (int)(sizeof(EvictShared) + 4u * (size_t)kKeysPerBlock), dev, done);
+  // When the clusters leave much of the GPU idle (8 of 16 blocks do, too: 7
+  // places hold one) and there can be many moves, a second kernel moves the
+  // rows, on all of it: 100000 of 300000 slots of one head 53 us against 118, 8
+  // heads of 131072 to 8192 42.5 against 44.1, 96 heads of 4096 to 2048 37.3
+  // against 38.0; but 128 heads of 4096 44.9 against 42.1, 10 heads of 131072
+  // 51.0 against 47.2, and up to 128 moves a head take 12.3 either way.
+  const int heads = B * Hkv, most = keep < cap - keep ? keep : cap - keep;
+  const bool split = heads * C <= (C == kMaxCluster ? sms : 2 * sms / 3) && most >= kSplitMoves * C;
+  p.moves = split ? reinterpret_cast<uint32_t*>(p.lists + (size_t)heads * cap) : nullptr;
+  auto* kernel = split ? evict_kernel<true> : evict_kernel<false>;
+  if (e == cudaSuccess && !done[split][dev])
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = allow_smem(kernel, (int)(sizeof(EvictShared) + 4u * (size_t)kKeysPerBlock), dev, done[split]);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * Hkv * C));
@@ -440,7 +481,10 @@ int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, c
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, evict_kernel, p));
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess || !split) return cuda_status(e);
+  const int blocks = ceil_div(2 * sms, heads);
+  return launch_after(evict_move_kernel, dim3((unsigned)(heads * blocks)), dim3(kEvThreads), 0, stream, p, blocks);
 }
 
 }  // namespace dhsa

@@ -297,22 +297,5 @@ struct Waits {
   }
 };
 
-// Launches a kernel that may start while the one before it on the stream
-// ends; the kernel itself waits (wait_for_predecessors) before it reads results.
-template <typename... P, typename... A>
-inline int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
-}
-
 }  // namespace
 }  // namespace dhsa
