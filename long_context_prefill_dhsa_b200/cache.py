@@ -64,7 +64,8 @@ class KVCache:
     A step of T new tokens (T = 1: decoding; more: a drafted tree) is
       q = cache.extend(Q, K, V, depth)     rotary positions; K, V into the slots after the cached ones
       O = cache.attend(q, parents)         attention over the cache and the step's own tokens
-      cache.commit(T, accept, keep)        accepted tokens stay, the rest is dropped; at most `keep` slots stay
+      cache.commit(T, accept, keep)        accepted tokens stay, the rest is dropped; at most `keep` slots stay,
+                                           the first `sinks` and the last `recent` positions first
 
     K, V [B,Hkv,cap,128], weight (fp32) and pos (int32) [B,Hkv,cap], lengths
     and next_pos (int32 [B]) are the state; every call runs on the current
@@ -153,14 +154,24 @@ class KVCache:
     def commit(self, n_draft: torch.Tensor, accept: Optional[torch.Tensor] = None, keep: Optional[int] = None):
         """End a step: of each sequence's n_draft (int32 [B]) new tokens those
         with their bit in accept (int64 [B]; None: all) stay, and of all slots
-        the `keep` (None: all) that rank first by held, weight, slot."""
+        the `keep` (None: all) that rank first by held, weight, slot. Held are
+        positions below `sinks`, the accepted tokens and the `recent`
+        positions before them; where these are more than `keep`, the sinks and
+        the last keep - sinks positions."""
         self._prompt = None
-        binding.cache_evict(self.K, self.V, self.weight, self.pos, self.lengths, self.cap if keep is None else keep,
-                            next_pos=self.next_pos, n_draft=n_draft, accept=accept, sinks=self.sinks,
-                            recent=self.recent, lengths_out=self._lengths_next, workspace=self._ws)
-        if accept is None:
-            self.next_pos += n_draft
-        else:
+        added = n_draft
+        if accept is not None:
             bit = (accept[:, None] >> self._bits) & (self._bits < n_draft[:, None])
-            self.next_pos += bit.sum(-1, dtype=torch.int32)
+            added = bit.sum(-1, dtype=torch.int32)
+        # cache_evict lets the lower slot win among held ones, and the newest
+        # tokens are in the highest: it must not be given more than `keep` of them
+        held_from, recent = self.next_pos, self.recent
+        if keep is not None and self.sinks + recent + self._bits.numel() > keep:
+            room = min(max(keep - self.sinks, 0), 0x7fffffff)
+            held_from = torch.maximum(self.next_pos - min(recent, 0x7fffffff), self.next_pos + added - room)
+            recent = 0
+        binding.cache_evict(self.K, self.V, self.weight, self.pos, self.lengths, self.cap if keep is None else keep,
+                            next_pos=held_from, n_draft=n_draft, accept=accept, sinks=self.sinks,
+                            recent=recent, lengths_out=self._lengths_next, workspace=self._ws)
+        self.next_pos += added
         self.lengths.copy_(self._lengths_next)      # the same tensor every step, so that a step can be captured
