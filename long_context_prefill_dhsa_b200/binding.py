@@ -498,6 +498,12 @@ def _evict_workspace(B: int, Hkv: int, cap: int) -> int:
     return load().dhsa_cache_evict_workspace_size(B, Hkv, cap)
 
 
+def _int32(x) -> int:
+    """A count as the library takes it: beyond 32 bits the nearest int (ctypes
+    would take it modulo 2^32, and "all" would become none)."""
+    return max(-0x80000000, min(int(x), 0x7fffffff))
+
+
 def _workspace(t: Optional[torch.Tensor], size: int, device: int):
     """Pointer and bytes of the caller's workspace, or of a new one (kept by the returned tensor)."""
     if t is None:
@@ -662,13 +668,13 @@ def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: tor
         pos_out = pos
     if lengths_out is None:
         lengths_out = torch.empty_like(lengths)
-    keep = min(int(keep), 0x7fffffff)
+    keep, sinks, recent = _int32(keep), _int32(sinks), _int32(recent)
     workspace, ws, ws_bytes = _workspace(workspace, _evict_workspace(B, Hkv, cap), device)
     _check(load().dhsa_cache_evict(
         k, ks, v, vs, _on(weight, torch.float32, (B, Hkv, cap), "weight", device),
         _on(pos, torch.int32, (B, Hkv, cap), "pos", device), B, Hkv, cap, d,
         _on(lengths, torch.int32, (B,), "lengths", device), _on(n_draft, torch.int32, (B,), "n_draft", device),
-        _on(accept, torch.int64, (B,), "accept", device), keep, int(sinks), int(recent),
+        _on(accept, torch.int64, (B,), "accept", device), keep, sinks, recent,
         _on(next_pos, torch.int32, (B,), "next_pos", device),
         _on(weight_out, torch.float32, (B, Hkv, cap), "weight_out", device),
         _on(pos_out, torch.int32, (B, Hkv, cap), "pos_out", device),
