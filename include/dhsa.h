@@ -422,7 +422,8 @@ int dhsa_rotary_qkv(const void* Q, const int64_t* q_strides, const void* K, cons
  *             weight_out[s] = weight[s] + sum over the head's Hq/Hkv query
  *             heads and the drafted tokens of p_s; for a drafted token's slot
  *             the sum alone. weight_out may be weight. Weights want a
- *             scale of at least 1e-30.
+ *             scale from 1e-30 to 1e30.
+ *    softmax_scale  above 0, at most 2.3e38
  *    Rows t >= n_draft[b] of O and lse and the other slots of weight_out are
  *    left as they were. lengths[b] outside [0, cap] and n_draft[b] outside
  *    [0, T] or past the capacity are clamped (DHSA_DEVFLAG_BAD_CACHE); a

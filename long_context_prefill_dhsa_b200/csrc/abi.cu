@@ -449,9 +449,10 @@ int dhsa_tree_attn(const void* Q, const void* K, const int64_t* k_strides, const
   if ((long long)B * Hq * T > 0x7fffffffLL) return DHSA_ERR_INVALID_ARG;
   if (T > tree_max_drafts() || Hq / Hkv > tree_max_group()) return DHSA_ERR_UNSUPPORTED;
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return DHSA_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.f) || softmax_scale - softmax_scale != 0.f) return DHSA_ERR_INVALID_ARG;
-  // a slot's weight subtracts log(denominator) / scale from its scores: this has to fit
-  if (weight && softmax_scale < 1e-30f) return DHSA_ERR_INVALID_ARG;
+  // finite in powers of two, too: inf times the difference 0 of the best score would be NaN
+  if (!(softmax_scale > 0.f) || !(softmax_scale <= 2.3e38f)) return DHSA_ERR_INVALID_ARG;
+  // a slot's weight subtracts log(denominator) / scale from its scores: this has to fit, and not to be denormal
+  if (weight && (softmax_scale < 1e-30f || softmax_scale > 1e30f)) return DHSA_ERR_INVALID_ARG;
   RowStrides ks, vs;
   if (!read_strides(k_strides, B, Hkv, cap, true, &ks) || !read_strides(v_strides, B, Hkv, cap, true, &vs))
     return DHSA_ERR_INVALID_ARG;
