@@ -11,10 +11,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import importlib
+import importlib.util
 import math
 import os
 import re
+import warnings
 from typing import Optional
 
 import torch
@@ -99,15 +100,33 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+class _ChecksInPython:
+    """Stands in for the compiled checks where they are not built for this torch and Python."""
+
+    @staticmethod
+    def _leave(*args):
+        return None
+
+    rotary_qkv = tree_attn = cache_evict = _leave
+
+
 def _load_marshal():
-    """Load _marshal.so (csrc/marshal.cpp), which checks the arguments of the
-    cache's calls and makes them, for the library that load() has."""
+    """Load the compiled checks (csrc/marshal.cpp) of the cache's calls, which
+    make them, for the library that load() has. Without a file for this very
+    torch and Python the same checks run in Python, a few us a call slower."""
     global _marshal
     if _marshal is None:
+        from . import build
         lib = load()
-        if not os.path.exists(os.path.join(_PKG, "_marshal.so")):
-            raise RuntimeError("_marshal.so is missing: build it with `python -m long_context_prefill_dhsa_b200.build`")
-        m = importlib.import_module(__package__ + "._marshal")
+        path = build.marshal_path()
+        if not os.path.exists(path):
+            warnings.warn(f"{path} is missing, arguments are checked in Python: build it with "
+                          "`python -m long_context_prefill_dhsa_b200.build`")
+            _marshal = _ChecksInPython
+            return _marshal
+        spec = importlib.util.spec_from_file_location(__package__ + "._marshal", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.dhsa_rotary_qkv, lib.dhsa_tree_attn, lib.dhsa_tree_attn_workspace_size, lib.dhsa_cache_evict,
             lib.dhsa_cache_evict_workspace_size)))

@@ -1,15 +1,19 @@
 """Build libdhsa.so (the C-ABI library) in-tree with nvcc for sm_100a, and
-_marshal.so (the Python binding's argument checks) with g++.
+the Python binding's argument checks (csrc/marshal.cpp) with g++.
 
     python -m long_context_prefill_dhsa_b200.build [--verbose-ptxas] [--force]
 
 Objects go to long_context_prefill_dhsa_b200/_build/, the shared libraries
 next to this file. A rebuild happens only when a source or header is newer
-than the libraries (or with --force).
+than the libraries (or with --force). The library needs nvcc alone, and is
+built whatever becomes of the checks; those read tensors in torch's own layout,
+so their file's name says for which torch and Python they were built, and no
+other opens it. Without torch they are not built.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -22,7 +26,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdhsa.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+HEADER = os.path.join(ROOT, "include", "dhsa.h")
 SOURCES = ["abi.cu", "pool.cu", "score_topk.cu", "csr.cu", "items.cu", "attn.cu", "attn_fwd.cu", "attn_short.cu",
            "rotary.cu", "tree_attn.cu", "tree_weight.cu", "tree_join.cu", "evict.cu"]
 HEADERS = ["common.cuh", "sm100_ptx.cuh", "tmap.cuh", "pool_row.cuh", "cache.cuh",
@@ -37,22 +41,25 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + ["marshal.cpp"]]
-    files.append(os.path.join(ROOT, "include", "dhsa.h"))
-    return files
+def marshal_path() -> str:
+    """Where the binding's compiled checks for this torch and Python are."""
+    return os.path.join(PKG, f"_marshal-torch{importlib.metadata.version('torch')}"
+                             f"-{sysconfig.get_config_var('SOABI')}.so")
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+def _newer_than(path: str, files) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in files)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+def library_up_to_date() -> bool:
+    return _newer_than(LIB, [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [HEADER])
+
+
+def marshal_up_to_date() -> bool:
+    return _newer_than(marshal_path(), [os.path.join(CSRC, "marshal.cpp"), HEADER])
+
+
+def build_library(verbose_ptxas: bool = False):
     os.makedirs(OBJ, exist_ok=True)
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
                     "-I", os.path.join(ROOT, "include")]
@@ -65,24 +72,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    def compile_marshal():
-        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
-        tmp = MARSHAL + ".tmp"
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, os.path.join(CSRC, "marshal.cpp")]
-        for d in (os.path.join(ROOT, "include"), os.path.join(torch, "include"),
-                  os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
-                  os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")):
-            cmd += ["-I", d]
-        cmd += ["-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
-        return tmp
-
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(compile_marshal)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        marshal = marshal.result()
     for src, _, r in results:
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
@@ -94,7 +85,35 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    os.replace(marshal, MARSHAL)
+
+
+def build_marshal():
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    path = marshal_path()
+    tmp = path + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, os.path.join(CSRC, "marshal.cpp")]
+    for d in (os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+              os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+              os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")):
+        cmd += ["-I", d]
+    cmd += ["-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+    os.replace(tmp, path)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """Builds what is not up to date. A failure of the checks is raised after
+    the library is in place."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = None
+        if importlib.util.find_spec("torch") is not None and (force or not marshal_up_to_date()):
+            marshal = ex.submit(build_marshal)
+        if force or not library_up_to_date():
+            build_library(verbose_ptxas)
+        if marshal is not None:
+            marshal.result()
     return LIB
 
 
