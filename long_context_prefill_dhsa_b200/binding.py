@@ -809,6 +809,11 @@ class HostStreamedPrefill:
     two copy directions use the two PCIe directions). Returns at once;
     synchronize() waits for every submitted layer. Host buffers must stay
     untouched until then.
+
+    A layer with inv_freq keeps its rotated K only until the next one is
+    submitted: submit(..., cache=) fills that layer's KVCache with it and V, on
+    the compute stream, after what the current stream has done to the cache.
+    No other stream may use the cache before synchronize().
     """
 
     def __init__(self, layer: DHSAPrefill):
@@ -825,7 +830,7 @@ class HostStreamedPrefill:
         self.e_out = [torch.cuda.Event() for _ in range(2)]
         self.n = 0
 
-    def submit(self, Qh: torch.Tensor, Kh: torch.Tensor, Vh: torch.Tensor, Oh: torch.Tensor):
+    def submit(self, Qh: torch.Tensor, Kh: torch.Tensor, Vh: torch.Tensor, Oh: torch.Tensor, cache=None):
         b = self.n & 1
         lay = self.layer
         if self.n >= 2:
@@ -838,8 +843,12 @@ class HostStreamedPrefill:
         self.s_comp.wait_event(self.e_in[b])
         if self.n >= 2:
             self.s_comp.wait_event(self.e_out[b])      # layer n-2's O has left this buffer
+        if cache is not None:
+            self.s_comp.wait_stream(torch.cuda.current_stream(self.s_comp.device))
         with torch.cuda.stream(self.s_comp):
             Q, K = lay.rotate(self.Qd[b], self.Kd[b])
+            if cache is not None:
+                cache.fill(K, self.Vd[b])
             lay.routing(Q, K)
             sparse_attn_fwd(Q, K, self.Vd[b], lay.off, lay.n_chunks, lay.row_ptr, lay.col_idx,
                             lay.cost, lay.scale, out=self.Od[b], workspace=lay.ws_attn)
