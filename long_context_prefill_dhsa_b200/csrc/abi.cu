@@ -1,5 +1,6 @@
 // extern "C" entry points of libdhsa: host-side argument checks, then the
 // stage launchers. Every check happens before anything is enqueued.
+#include <atomic>
 #include <cstring>
 
 #include "cache.cuh"
@@ -59,8 +60,9 @@ namespace {
 __device__ unsigned int g_device_status = 0;
 thread_local int t_last_cuda_error = 0;
 constexpr int kMaxDevices = 64;
-unsigned int* g_status_ptr[kMaxDevices] = {nullptr};
-int g_sm100[kMaxDevices] = {0};  // 0 unknown, 1 yes, -1 no
+// atomics: host threads may make their first calls at the same time
+std::atomic<unsigned int*> g_status_ptr[kMaxDevices];
+std::atomic<int> g_sm100[kMaxDevices];  // 0 unknown, 1 yes, -1 no
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 }  // namespace

@@ -1,6 +1,8 @@
 // Shared by the calls on a key/value cache (rotary.cu, tree_attn.cu, evict.cu):
 // row strides, and the clamped view of a sequence's lengths.
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 #include "tmap.cuh"
 
@@ -44,27 +46,30 @@ inline bool make_cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What is looked up or set once per device is kept in atomics: host threads
+// may make their first calls at the same time, and then find the same values.
+
 // The current device's number and SM count, looked up once per device.
 inline cudaError_t this_device(int* dev, int* sms) {
   constexpr int kMost = 64;
-  static int count[kMost] = {0};
+  static std::atomic<int> count[kMost];
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return e;
   if (*dev < 0 || *dev >= kMost) return cudaErrorInvalidDevice;
-  if (count[*dev] == 0) {
-    int n = 0;
+  int n = count[*dev];
+  if (n == 0) {
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
     if (e != cudaSuccess) return e;
     count[*dev] = n;
   }
-  *sms = count[*dev];
+  *sms = n;
   return cudaSuccess;
 }
 
 // Raises a kernel's dynamic shared memory limit, once per device and kernel
 // (`done`: a static array of 64 flags beside the launch).
 template <typename F>
-inline cudaError_t allow_smem(F* kernel, int bytes, int dev, bool* done) {
+inline cudaError_t allow_smem(F* kernel, int bytes, int dev, std::atomic<bool>* done) {
   if (done[dev]) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done[dev] = true;

@@ -452,7 +452,7 @@ int launch_evict(void* K, const RowStrides& ks, void* V, const RowStrides& vs, c
   const int span = ceil_div(cap, C * kEvThreads) * kEvThreads;   // slots of one block at most
   p.keys_held = span <= kKeysPerBlock ? span : kKeysOfMore;
   const size_t smem = sizeof(EvictShared) + 4u * (size_t)p.keys_held;
-  static bool done[2][64] = {{false}};
+  static std::atomic<bool> done[2][64];
   int dev = 0, sms = 0;
   cudaError_t e = this_device(&dev, &sms);
   // When the clusters leave much of the GPU idle (8 of 16 blocks do, too: 7

@@ -5,6 +5,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace dhsa {
@@ -16,13 +18,14 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 // The driver's tensor-map encoder, looked up once through the runtime (no
 // link-time dependency on libcuda).
 inline EncodeTiledFn tmap_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
+  static std::atomic<EncodeTiledFn> found{nullptr};
+  EncodeTiledFn fn = found;
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+      found = fn = reinterpret_cast<EncodeTiledFn>(ptr);
   }
   return fn;
 }

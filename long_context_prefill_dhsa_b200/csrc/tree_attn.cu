@@ -645,7 +645,7 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   TreeMaps maps;
   if (!make_cache_map(enc, &maps.k, K, ks, B, Hkv, cap, BN) || !make_cache_map(enc, &maps.v, V, vs, B, Hkv, cap, BN))
     return DHSA_ERR_INVALID_ARG;
-  static bool done[3][64] = {{false}};
+  static std::atomic<bool> done[3][64];
   int dev = 0, sms = 0;
   cudaError_t e = this_device(&dev, &sms);
   // Rows beyond 64 need both halves of the lanes of each quarter; up to 64,

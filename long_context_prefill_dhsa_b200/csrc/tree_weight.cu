@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
 }  // namespace
 
 int launch_tree_weight(const CUtensorMap& k, const TreeParams& p, cudaStream_t stream) {
-  static bool done[64] = {false};
+  static std::atomic<bool> done[64];
   int dev = 0, sms = 0;
   cudaError_t e = this_device(&dev, &sms);
   if (e == cudaSuccess) e = allow_smem(tree_weight_kernel, (int)kSmemAlloc, dev, done);
