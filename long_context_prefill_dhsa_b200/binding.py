@@ -179,8 +179,9 @@ def check_device_status() -> int:
 
 def debug_arm_wait_timeout(mode: int, limit_ns: int = 0):
     """Test hook of the bounded device waits (include/dhsa.h, 5): mode 1 makes
-    the next attention launch's first waits run out after limit_ns, mode 2
-    the next fused-routing launch's first grid barrier; 0 disarms."""
+    the next attention call's first waits run out after limit_ns (the
+    prefill's or that of drafted tokens), mode 2 the next fused-routing
+    launch's first grid barrier; 0 disarms."""
     _check(load().dhsa_debug_arm_wait_timeout(mode, limit_ns), "dhsa_debug_arm_wait_timeout")
 
 

@@ -30,6 +30,8 @@ struct TreeParams {
   bool every;               // sequences without drafted tokens are walked too
   float scale, scale_log2;
   unsigned int* status;
+  unsigned long long wait_limit_ns;
+  bool hold;                // test hook: no tile is loaded, so that the waits for the first ones run out
 };
 
 namespace {
@@ -283,13 +285,15 @@ __device__ __forceinline__ Sees tree_sees(const TreeParams& p, int b, int draft,
   return s;
 }
 
+// As in attn_fwd.cu: the lanes that wait together poll in lockstep and give up together.
 struct Waits {
   volatile int* abort;
   unsigned int* status;
+  unsigned long long limit_ns;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_test_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (mbar_wait_slow(bar, parity, kWaitLimitNs)) return true;
+    if (mbar_wait_slow(bar, parity, limit_ns)) return true;
     if (mbar_test_wait(bar, parity)) return true;
     *abort = 1;
     raise_device_flag(status, DHSA_DEVFLAG_WAIT_TIMEOUT);

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR), 0);
     share = *line;
   }
-  const Waits wait{abort_flag, p.status};
+  const Waits wait{abort_flag, p.status, p.wait_limit_ns};
   Pieces walk{share.start, share.end, share.base, share.b};
   Piece w{};
 
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
       const uint64_t v_policy = p.blocks > 1 ? l2_evict_normal() : l2_evict_first();
       const uint64_t k_policy = p.keep_k || p.blocks > 1 ? l2_evict_normal() : l2_evict_first();
       uint32_t g = 0;     // tiles loaded
-      bool ok = true;
+      bool ok = !p.hold;
       auto load = [&](const CUtensorMap* m, int tile) {
         const uint32_t st = g % NST;
         if (g >= NST && !wait(bar(B_EMPTY + st), (g / NST - 1) & 1)) return false;
@@ -693,6 +693,8 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = status;
+  p.wait_limit_ns = kWaitLimitNs;
+  p.hold = take_wait_test(1, &p.wait_limit_ns);      // test hook: the first waits run out
   kernel<<<p.grid, block_threads(halves), kSmemAlloc, stream>>>(maps, p);
   int st = launch_status();
   if (st == DHSA_OK && q.scores) {

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR), 0);
-  const Waits wait{abort_flag, p.status};
+  const Waits wait{abort_flag, p.status, p.wait_limit_ns};
   Pieces walk{line->start, line->end, line->base, line->b};
   Piece w{};
   const int walks = (p.rows + kRowBlock - 1) / kRowBlock;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   if (warp == 0) {
     if (lane == 0) {
       uint32_t g = 0;
-      bool ok = true;
+      bool ok = !p.hold;
       const uint64_t usual = l2_evict_normal(), last = l2_evict_first();
       while (ok && walk.next(p, &w)) {
         for (int rb = 0; ok && rb < walks; ++rb)
