@@ -357,7 +357,8 @@ int dhsa_sparse_attn_fwd_tiles(const void* Q, const void* K, const void* V, int 
  *              the CTAs record the flag, free their TMEM and return without
  *              writing O. The next call of 7., if that comes first: none of its
  *              kernels loads a key tile, so the waits for the first one run
- *              out; rows and weights that a joining kernel writes mean nothing.
+ *              out (after limit_ns, rounded up to a power of two); rows and
+ *              weights that a joining kernel writes mean nothing.
  *      mode 2: the next one-launch routing (2c., 2d.) has block 0 arrive
  *              late at its first grid barrier; the other blocks give up
  *              after limit_ns, set the abort word, and all blocks leave.

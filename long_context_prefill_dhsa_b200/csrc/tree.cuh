@@ -28,10 +28,9 @@ struct TreeParams {
   bool whole;               // items are not split: the line counts items instead of key tiles
   bool keep_k;              // K is read again after this kernel
   bool every;               // sequences without drafted tokens are walked too
+  uint8_t hold;             // test hook, if not 0: no tile is loaded, and waits run out after 2^hold ns
   float scale, scale_log2;
   unsigned int* status;
-  unsigned long long wait_limit_ns;
-  bool hold;                // test hook: no tile is loaded, so that the waits for the first ones run out
 };
 
 namespace {
@@ -287,13 +286,12 @@ __device__ __forceinline__ Sees tree_sees(const TreeParams& p, int b, int draft,
 
 // As in attn_fwd.cu: the lanes that wait together poll in lockstep and give up together.
 struct Waits {
-  volatile int* abort;
+  volatile int* abort;      // [1]: the limit in ns
   unsigned int* status;
-  unsigned long long limit_ns;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_test_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (mbar_wait_slow(bar, parity, limit_ns)) return true;
+    if (mbar_wait_slow(bar, parity, (unsigned)abort[1])) return true;
     if (mbar_test_wait(bar, parity)) return true;
     *abort = 1;
     raise_device_flag(status, DHSA_DEVFLAG_WAIT_TIMEOUT);

@@ -96,7 +96,7 @@ constexpr uint32_t OFF_XCHG = OFF_SEE + kMaxDrafts * 8;            // per row of
 constexpr uint32_t OFF_LINE = OFF_XCHG + BM * 8;
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;   // slack for aligning the base
+constexpr uint32_t kSmemAlloc = OFF_ABORT + 8 + 1024;   // slack for aligning the base
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 static_assert(sizeof(Line) % 8 == 0, "alignment");
 static_assert(BN == kTileSlots && BM == kTileRows, "the line is cut into these tiles");
@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (warp == W_PRODUCER && lane == 0) {
-    *abort_flag = 0;
+    abort_flag[0] = 0;
+    abort_flag[1] = p.hold ? 1 << p.hold : (int)kWaitLimitNs;
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(B_FULL + s), 1);
       mbar_init(bar(B_EMPTY + s), 1);
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
     tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR), 0);
     share = *line;
   }
-  const Waits wait{abort_flag, p.status, p.wait_limit_ns};
+  const Waits wait{abort_flag, p.status};
   Pieces walk{share.start, share.end, share.base, share.b};
   Piece w{};
 
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(block_threads(HALVES), 1) tree_attn_kernel(con
       const uint64_t v_policy = p.blocks > 1 ? l2_evict_normal() : l2_evict_first();
       const uint64_t k_policy = p.keep_k || p.blocks > 1 ? l2_evict_normal() : l2_evict_first();
       uint32_t g = 0;     // tiles loaded
-      bool ok = !p.hold;
+      bool ok = p.hold == 0;
       auto load = [&](const CUtensorMap* m, int tile) {
         const uint32_t st = g % NST;
         if (g >= NST && !wait(bar(B_EMPTY + st), (g / NST - 1) & 1)) return false;
@@ -693,8 +694,10 @@ int launch_tree_attn(const void* Q, const void* K, const RowStrides& ks, const v
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = status;
-  p.wait_limit_ns = kWaitLimitNs;
-  p.hold = take_wait_test(1, &p.wait_limit_ns);      // test hook: the first waits run out
+  unsigned long long limit_ns;
+  p.hold = 0;
+  if (take_wait_test(1, &limit_ns))      // test hook: the first waits run out
+    while (1ull << ++p.hold < limit_ns) {}
   kernel<<<p.grid, block_threads(halves), kSmemAlloc, stream>>>(maps, p);
   int st = launch_status();
   if (st == DHSA_OK && q.scores) {

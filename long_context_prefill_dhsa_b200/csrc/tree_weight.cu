@@ -54,7 +54,7 @@ constexpr uint32_t OFF_BAR = OFF_XSUM + 4 * BN * 4;
 constexpr uint32_t OFF_LINE = OFF_BAR + 8 * ((W_COUNT + 1) & ~1);
 constexpr uint32_t OFF_TMEMPTR = OFF_LINE + sizeof(Line);
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-constexpr uint32_t kSmemAlloc = OFF_ABORT + 4 + 1024;
+constexpr uint32_t kSmemAlloc = OFF_ABORT + 8 + 1024;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory budget");
 static_assert(BN == kTileSlots, "the line is cut into these tiles");
 
@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
 
   if (warp == 0) {
     if (lane == 0) {
-      *abort_flag = 0;
+      abort_flag[0] = 0;
+      abort_flag[1] = p.hold ? 1 << p.hold : (int)kWaitLimitNs;
       for (int s = 0; s < kStages; ++s) {
         mbar_init(bar(W_FULL + s), 1);
         mbar_init(bar(W_EMPTY + s), 1);
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEMPTR), 0);
-  const Waits wait{abort_flag, p.status, p.wait_limit_ns};
+  const Waits wait{abort_flag, p.status};
   Pieces walk{line->start, line->end, line->base, line->b};
   Piece w{};
   const int walks = (p.rows + kRowBlock - 1) / kRowBlock;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_weight_kernel(const __grid_c
   if (warp == 0) {
     if (lane == 0) {
       uint32_t g = 0;
-      bool ok = !p.hold;
+      bool ok = p.hold == 0;
       const uint64_t usual = l2_evict_normal(), last = l2_evict_first();
       while (ok && walk.next(p, &w)) {
         for (int rb = 0; ok && rb < walks; ++rb)
