@@ -291,7 +291,11 @@ struct Waits {
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_test_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (mbar_wait_slow(bar, parity, (unsigned)abort[1])) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((it & 15u) == 0u && globaltimer_ns() - t0 > (unsigned)abort[1]) break;
+    }
     if (mbar_test_wait(bar, parity)) return true;
     *abort = 1;
     raise_device_flag(status, DHSA_DEVFLAG_WAIT_TIMEOUT);
