@@ -452,7 +452,8 @@ int dhsa_tree_attn(const void* Q, const void* K, const int64_t* k_strides, const
  *    Candidates of sequence b: slots s < lengths[b], and slots lengths[b] + j
  *    for j < n_draft[b] with bit j of accept[b] set (accept NULL: all; n_draft
  *    NULL: none). m = min(keep, candidates). Each kv head keeps its own m
- *    candidates, ranked by (held first, weight descending, slot ascending);
+ *    candidates: first the held ones, the lower slots first whatever their
+ *    weights, then the others by (weight descending, slot ascending);
  *    held: pos < sinks or pos >= next_pos[b] - recent (next_pos NULL: recent
  *    must be 0). A NaN weight ranks below every number; -0 equals +0.
  *

@@ -665,7 +665,8 @@ def cache_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, pos: tor
     weight fp32 and pos int32 [B,Hkv,cap] (updated in place unless weight_out
     and pos_out are given); n_draft int32 [B] drafted slots after `lengths`,
     of which those with their bit in accept (int64 [B]; None: all) may stay.
-    Slots with pos < sinks or pos >= next_pos - recent rank first. index
+    Slots with pos < sinks or pos >= next_pos - recent rank first, the lower
+    slot first among them if they are more than `keep`. index
     (int32 [B,Hkv,min(keep,cap)]) receives each slot's source.
     Returns lengths_out (a new tensor unless given; not `lengths` itself)."""
     done = (_marshal or _load_marshal()).cache_evict(K, V, weight, pos, lengths, keep, next_pos, n_draft, accept, sinks,

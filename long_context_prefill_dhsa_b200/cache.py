@@ -154,7 +154,7 @@ class KVCache:
     def commit(self, n_draft: torch.Tensor, accept: Optional[torch.Tensor] = None, keep: Optional[int] = None):
         """End a step: of each sequence's n_draft (int32 [B]) new tokens those
         with their bit in accept (int64 [B]; None: all) stay, and of all slots
-        the `keep` (None: all) that rank first by held, weight, slot. Held are
+        the `keep` (None: all) that rank first by held, then weight, slot. Held are
         positions below `sinks`, the accepted tokens and the `recent`
         positions before them; where these are more than `keep`, the sinks and
         the last keep - sinks positions."""

@@ -1,8 +1,8 @@
 // Eviction from a key/value cache by accumulated attention weight, and the
 // commit of accepted drafts (the same update with room for every candidate).
 //
-// Each (sequence, kv head) keeps the m candidates that rank first by (held,
-// weight descending, slot ascending). The rank is a 32-bit key whose unsigned
+// Each (sequence, kv head) keeps the m candidates that rank first: the held
+// ones by slot, then the others by (weight descending, slot ascending). The rank is a 32-bit key whose unsigned
 // order is that of the weights; held slots take the largest key, slots that
 // are no candidates the key 0. The m-th largest key is found by a radix
 // search (four 8-bit digits from the top, one histogram each); among equal
