@@ -2,11 +2,11 @@
 // commit of accepted drafts (the same update with room for every candidate).
 //
 // Each (sequence, kv head) keeps the m candidates that rank first: the held
-// ones by slot, then the others by (weight descending, slot ascending). The rank is a 32-bit key whose unsigned
-// order is that of the weights; held slots take the largest key, slots that
-// are no candidates the key 0. The m-th largest key is found by a radix
-// search (four 8-bit digits from the top, one histogram each); among equal
-// keys the first slots win.
+// ones by slot, then the others by (weight descending, slot ascending). The
+// rank is a 32-bit key whose unsigned order is that of the weights; held slots
+// take the largest key, slots that are no candidates the key 0. The m-th
+// largest key is found by a radix search (four 8-bit digits from the top, one
+// histogram each); among equal keys the first slots win.
 //
 // The kept rows must end in slots 0 .. m-1, and the order of slots carries no
 // meaning, so only as many rows move as there are unkept slots below m: the
@@ -16,8 +16,8 @@
 // One thread-block cluster per (sequence, head): its blocks split the slots,
 // hold the keys in shared memory, and read each other's histograms and
 // counts through distributed shared memory, so the whole update is one
-// launch (two when few heads have many rows to move). Bound: 8 bytes (weight, position) per slot and 1 KB per moved row
-// against HBM; for small caches the chain of four histogram rounds, one round
+// launch (two when few heads have many rows to move). Bound: 8 bytes (weight,
+// position) per slot and 1 KB per moved row against HBM; for small caches the chain of four histogram rounds, one round
 // of counts and their barriers. Measured: 8 heads of 131072 slots to 8192, 42.5
 // us, 27 of them ranking (about 6 us until the keys are there, 3 a round, 10
 // for counts and lists) and 12 moving 61K rows (63 MB at 5.3 TB/s).
@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_move_kernel(const EvictPa
 // rounds between them: 8 heads of 131072 slots take 49.7 us with 8, 44.9 with
 // 10 and 43.6 with 16; 256 heads of 4112 slots 16.1 us with one block and 23.5
 // with two. Of clusters of 16, 14 run at a time: 12 heads of 131072 slots take
-// 47.3 us with 16 and 53.3 with 8, 16 heads 78 and 65.
+// 47.3 us with 16 and 53.3 with 8, 16 heads 78 and 65. (The capacity decides,
+// as the lengths are not known on the host: 8 heads with 8208 slots in use take
+// 20.5 us in a cache of 131136 slots and 13.3 in one of 8208.)
 int cluster_size(int cap, int heads) {
   int c = 1;
   while (c < kMaxCluster && (long long)c * kSlotsPerBlock < cap && (c < 8 || heads <= kLargeClusters)) c *= 2;

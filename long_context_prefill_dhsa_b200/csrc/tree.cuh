@@ -44,7 +44,9 @@ constexpr int kMaxGroup = 64;    // query heads of one kv head
 // again from K. Kept against computed again, us, 32/8 heads: one sequence of
 // 131000 slots with 8, 16, 24, 32 rows 104, 119, 134, 150 against 168 to 171;
 // 16 of 4000 to 8000 slots 83, 92, -, 118 against 163 to 166. Each further row
-// adds about 2 us at 128K, so the two meet near 44 rows.
+// adds about 2 us at 128K, so the two would meet near 42 rows. (33 to 42 take the
+// longer way: the joining blocks have statistics for 32 rows, four a warp, and
+// no limit between the two has been measured.)
 constexpr int kMaxScoreRows = 32;
 constexpr int kMaxGrid = 160;    // CTAs (one per SM) the workspace is sized for
 

@@ -8,9 +8,9 @@
 // value is read from HBM once: 512 bytes per slot against 512 FLOP per slot
 // and row. Up to about 250 rows HBM is the bound, above them the tensor cores
 // and the exponentials. Measured (32/8 heads, joining included): one token over
-// 131071 slots 89.6 us, 537 MB at 6.0 TB/s; 64 tokens over 131008 slots 144 us,
-// 137 GFLOP at 950 TFLOP/s, where each stream waits in turn for its scores and
-// for its exponentials (tensor cores 41% busy, special-function units 42%).
+// 131071 slots 89.6 us, 537 MB at 6.0 TB/s; 64 tokens over 131008 slots 145 us,
+// 137 GFLOP at 945 TFLOP/s, where each stream waits in turn for its scores and
+// for its exponentials (over 40000 slots tensor cores 41% busy, special-function units 42%).
 //
 // sm_100a design
 // --------------
