@@ -43,8 +43,11 @@ def nvcc() -> str:
 
 def marshal_path() -> str:
     """Where the binding's compiled checks for this torch and Python are."""
-    return os.path.join(PKG, f"_marshal-torch{importlib.metadata.version('torch')}"
-                             f"-{sysconfig.get_config_var('SOABI')}.so")
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:      # run from its source tree, say
+        from torch import __version__ as torch
+    return os.path.join(PKG, f"_marshal-torch{torch}-{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _newer_than(path: str, files) -> bool:
@@ -106,14 +109,15 @@ def build_marshal():
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Builds what is not up to date. A failure of the checks is raised after
     the library is in place."""
-    with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        marshal = None
+    def checks():
         if importlib.util.find_spec("torch") is not None and (force or not marshal_up_to_date()):
-            marshal = ex.submit(build_marshal)
+            build_marshal()
+
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = ex.submit(checks)
         if force or not library_up_to_date():
             build_library(verbose_ptxas)
-        if marshal is not None:
-            marshal.result()
+        marshal.result()
     return LIB
 
 

@@ -47,6 +47,15 @@ def test_checks_of_another_torch_or_python_are_out_of_date(monkeypatch):
     assert build.marshal_path() != here and not build.marshal_up_to_date()
 
 
+def test_a_torch_without_package_metadata(made, monkeypatch):
+    here = build.marshal_path()
+
+    def none(name):
+        raise build.importlib.metadata.PackageNotFoundError(name)
+    monkeypatch.setattr(build.importlib.metadata, "version", none)
+    assert build.marshal_path() == here and build.build() == build.LIB and "library" in made
+
+
 def test_checks_of_another_torch_are_not_loaded(monkeypatch):
     """The binding then checks in Python, says so, and refuses as before."""
     build.build()
