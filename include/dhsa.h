@@ -37,6 +37,8 @@
  *   call takes `*_strides`, that is a HOST pointer to three int64 (batch, head,
  *   row; in elements), or NULL for the dense layout. Rows are contiguous;
  *   strides are multiples of 8 elements and base pointers 16-byte aligned.
+ *   The Q, K, V that 6. reads may repeat (stride 0); in caches and outputs a
+ *   dimension of more than one entry has a stride of a row or more.
  *     cache K, V  bf16 [B, Hkv, cap, 128]   slot s of kv head h of sequence b
  *     lengths     int32 [B]  slots 0 .. lengths[b]-1 hold keys; the drafted
  *                            tokens of a step sit in the slots right after
