@@ -84,3 +84,44 @@ def test_the_newest_tokens_stay_when_the_budget_is_what_is_held(lib, case, track
                 assert sorted(pos) == want, (step, b, h)
                 for s, p in enumerate(pos):
                     assert torch.equal(c.K[b, h, s], at[b][p][0][h]) and torch.equal(c.V[b, h, s], at[b][p][1][h])
+
+
+@needs_gpu
+def test_a_captured_step_with_a_budget_of_what_is_held(lib):
+    """A drafted step captured once and replayed with other drafts and other accepted ones."""
+    from long_context_prefill_dhsa_b200 import cache
+    sinks, recent, keep, T, B, Hq, Hkv, L = 4, 8, 12, 5, 2, 4, 2, 40
+    rng = np.random.default_rng(62)
+    f, m = cache.rotary_inv_freq(128)
+    c = cache.KVCache(B, Hq, Hkv, 64, f, rotary_factor=m, sinks=sinks, recent=recent)
+    q, k, v = _bf(rng, B, Hq, T, D), _bf(rng, B, Hkv, T, D), _bf(rng, B, Hkv, T, D)
+    n_new, accept = _i32([T] * B), torch.zeros(B, dtype=torch.int64, device="cuda")
+
+    def step():
+        c.attend(c.extend(q, k, v))
+        c.commit(n_new, accept=accept, keep=keep)
+
+    def start():
+        c.fill(prompt, prompt)
+        c.commit(_i32([0] * B), keep=keep)
+
+    prompt = _bf(rng, B, Hkv, L, D)
+    start()
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    start()
+    seen = [L] * B
+    for acc in ((5, 1), (0, 2), (3, 5), (1, 0), (5, 5)):
+        for x in (q, k, v):
+            x.copy_(_bf(rng, *x.shape))
+        accept.copy_(torch.tensor([(1 << a) - 1 for a in acc], device="cuda"))
+        g.replay()
+        for b in range(B):
+            seen[b] += acc[b]
+            want = list(range(sinks)) + list(range(seen[b] - recent, seen[b]))
+            for h in range(Hkv):
+                assert sorted(c.pos[b, h, : int(c.lengths[b])].tolist()) == want
+    assert c.next_pos.tolist() == seen
